@@ -8,12 +8,12 @@
 #include <cstdio>
 #include <cstring>
 
-#include "../../include/mxfp8.h"
+#include "mx_abi_common.h"
 #include "mx_kernels.h"
 
-namespace {
+namespace mxabi {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 mx_status fail(mx_status st, const char* fmt, ...) {
   va_list ap;
@@ -23,16 +23,8 @@ mx_status fail(mx_status st, const char* fmt, ...) {
   return st;
 }
 
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-// The GEMMs address a K128 scale matrix with 32-bit buffer offsets.
-bool scales_fit(int64_t rows, int64_t k) { return rows * (k / 32) < (1ll << 31); }
-// A GEMM tile's 256 operand rows of K codes are addressed with 32-bit offsets.
-bool k_fits(int64_t k) { return k * 256 < (1ll << 31); }
-
 // 0 = unknown, 1 = gfx950, -1 = other
-int g_dev_ok[64];
+static int g_dev_ok[64];
 
 mx_status check_device() {
   int dev = -1;
@@ -54,26 +46,24 @@ mx_status launched(hipError_t e, const char* what) {
   return MX_OK;
 }
 
-hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
+}  // namespace mxabi
+
+using namespace mxabi;
+
+namespace {
+
+// The GEMMs address a K128 scale matrix with 32-bit buffer offsets.
+bool scales_fit(int64_t rows, int64_t k) { return rows * (k / 32) < (1ll << 31); }
+// A GEMM tile's 256 operand rows of K codes are addressed with 32-bit offsets.
+bool k_fits(int64_t k) { return k * 256 < (1ll << 31); }
 
 }  // namespace
-
-#define MX_REQUIRE(cond, st, ...) \
-  do {                            \
-    if (!(cond)) return fail(st, __VA_ARGS__); \
-  } while (0)
-
-#define MX_DEVICE()                          \
-  do {                                       \
-    mx_status st_ = check_device();          \
-    if (st_ != MX_OK) return st_;            \
-  } while (0)
 
 extern "C" {
 
 int mx_abi_version(void) { return 3; }
 
-const char* mx_last_error(void) { return g_err; }
+const char* mx_last_error(void) { return mxabi::g_err; }
 
 mx_status mx_init(void) {
   mx_status st = check_device();
@@ -177,7 +167,7 @@ mx_status mx_swiglu_quant_bwd(const void* dh, int64_t ld_dh, const void* a, cons
   MX_REQUIRE(dh && a && b, MX_ERR_NULL, "mx_swiglu_quant_bwd: dh/a/b NULL");
   MX_REQUIRE(al16(dh) && al16(a) && al16(b) && ld_ab >= hidden && ld_ab % 8 == 0 && ld_dh >= hidden &&
                  ld_dh % 8 == 0,
-             MX_ERR_ALIGN, "mx_swiglu_quant_bwd: inputs must be 16-byte aligned with ld >= hidden, ld % 8 == 0");
+             MX_ERR_ALIGN, "mx_swiglu_quant_bwd: inputs must be 16-byte aligned with ld >= hidden, ld %% 8 == 0");
   MX_REQUIRE(!dab_out || al16(dab_out), MX_ERR_ALIGN, "mx_swiglu_quant_bwd: dab_out must be 16-byte aligned");
   MX_DEVICE();
   mxk::SwigluBwdArgs k{static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(a),
@@ -192,12 +182,6 @@ static mx_status check_mx_operand(const char* fn, const char* name, const uint8_
   MX_REQUIRE(al4(s), MX_ERR_ALIGN, "%s: %s scales must be 4-byte aligned", fn, name);
   return MX_OK;
 }
-
-#define MX_CHECK(expr)              \
-  do {                              \
-    mx_status st_ = (expr);         \
-    if (st_ != MX_OK) return st_;   \
-  } while (0)
 
 mx_status mx_scaled_mm(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb,
                        int64_t M, int64_t N, int64_t K, mx_dtype out_dtype, void* out, int64_t ld_out,

@@ -201,6 +201,28 @@ __device__ __forceinline__ float e4m3_value(uint32_t c) {
   return __uint_as_float(__float_as_uint(v) | ((c & 0x80u) << 24));
 }
 
+// 2^(b - 127) as a float32, NaN for b = 0xFF.
+__device__ __forceinline__ float e8m0_f32(uint32_t b) {
+  return b == 0xFFu ? __uint_as_float(0x7FC00000u) : scale_f32(b);
+}
+
+// Values of 8 E4M3 codes (little-endian) under scale byte sb: gfx950's
+// v_cvt_pk_f32_fp8 (exact, NaN codes give NaN) times the scale (exact down to
+// float32's smallest subnormals: a code has 4 significant bits).
+__device__ __forceinline__ void e4m3_chunk_values(uint2 q, uint32_t sb, float (&f)[8]) {
+  const float sc = e8m0_f32(sb);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int w = (int)(i ? q.y : q.x);
+    const mx_f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
+    const mx_f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+    f[4 * i] = lo.x * sc;
+    f[4 * i + 1] = lo.y * sc;
+    f[4 * i + 2] = hi.x * sc;
+    f[4 * i + 3] = hi.y * sc;
+  }
+}
+
 // ---------------------------------------------------------------- misc
 
 // Quotient by a fixed divisor d >= 1 with a precomputed multiplier

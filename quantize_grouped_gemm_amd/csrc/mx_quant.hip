@@ -141,23 +141,6 @@ __global__ __launch_bounds__(kTileThreads) void k_swiglu_fwd(SwigluFwdArgs a) {
   tile_colq(lds, rows_valid, cols_valid, a.rceil, TileOut{a.q_col, a.s_col, a.rows, a.hidden, a.k128}, r0, c0);
 }
 
-// dA = dh*b*s*(1 + a*(1-s)), dB = dh*a*s with s = sigmoid(a), float32.
-__device__ __forceinline__ void swiglu_grad_f32(float dh, float a, float b, float& da,
-                                                float& db) {
-  const float s = sigmoid_f32(a);
-  da = (dh * b) * (s * (1.0f + a * (1.0f - s)));
-  db = dh * (a * s);
-}
-
-__device__ __forceinline__ void swiglu_grad_pair(uint32_t wdh, uint32_t wa, uint32_t wb,
-                                                 uint32_t& da2, uint32_t& db2) {
-  float da0, db0, da1, db1;
-  swiglu_grad_f32(bf16_lo(wdh), bf16_lo(wa), bf16_lo(wb), da0, db0);
-  swiglu_grad_f32(bf16_hi(wdh), bf16_hi(wa), bf16_hi(wb), da1, db1);
-  da2 = pack_bf16x2(da0, da1);
-  db2 = pack_bf16x2(db0, db1);
-}
-
 template <bool NT>
 __global__ __launch_bounds__(kTileThreads) void k_swiglu_bwd(SwigluBwdArgs a) {
   __shared__ uint4 lds[kTR * kTC / 8];
