@@ -11,6 +11,7 @@
 
 #include "mx_device.h"
 #include "mx_lm.h"
+#include "mx_row.h"
 #include "mx_tile.h"
 
 namespace mxk {
@@ -39,27 +40,24 @@ __global__ __launch_bounds__(kTileThreads) void k_swiglu_ck_fwd(SwigluCkArgs a) 
 }
 
 // Codes and scale bytes of the thread's chunks of a tile whose (0,0) is row
-// r0, column c0 of the checkpoint [rows, ld]; rows and columns outside the
-// valid region read as zeros.
+// r0, column c0 of the checkpoint [rows, ld]. Chunks outside the valid region
+// read its last row or column in their place (loads without a branch: with
+// one, the compiler carried the widened float32 values of all chunks through
+// it, 256 VGPRs); the caller drops what comes of them.
 __device__ __forceinline__ void tile_load_codes(uint2 (&q)[kTileChunks], uint32_t (&sb)[kTileChunks], const uint8_t* qp,
                                                 const uint8_t* sp, int64_t ld, int64_t rows, bool k128, int64_t r0,
                                                 int64_t c0, int rows_valid, int cols_valid) {
   const int t = threadIdx.x;
-  const int cc = t & 15;
+  const int64_t c = c0 + min((t & 15) * 8, cols_valid - 8);
 #pragma unroll
   for (int j = 0; j < kTileChunks; ++j) {
-    const int row = (t >> 4) + 16 * j;
-    q[j] = make_uint2(0, 0);
-    sb[j] = 0;
-    if (row < rows_valid && cc * 8 < cols_valid) {
-      const int64_t r = r0 + row, c = c0 + cc * 8;
-      q[j] = *reinterpret_cast<const uint2*>(qp + r * ld + c);
-      sb[j] = k128 ? sp[((c >> 7) * rows + r) * 4 + ((c >> 5) & 3)] : sp[r * (ld / kBlock) + (c >> 5)];
-    }
+    const int64_t r = r0 + min((t >> 4) + 16 * j, rows_valid - 1);
+    q[j] = *reinterpret_cast<const uint2*>(qp + r * ld + c);
+    sb[j] = sp[k128 ? ((c >> 7) * rows + r) * 4 + ((c >> 5) & 3) : r * (ld / kBlock) + (c >> 5)];
   }
 }
 
-__global__ __launch_bounds__(kTileThreads) void k_swiglu_ck_bwd(SwigluCkArgs a) {
+__global__ __launch_bounds__(kTileThreads, 4) void k_swiglu_ck_bwd(SwigluCkArgs a) {
   __shared__ uint4 lds[kTR * kTC / 8];
   const int64_t r0 = (int64_t)blockIdx.y * kTR;
   const int64_t c0 = (int64_t)blockIdx.x * kTC;
@@ -83,10 +81,12 @@ __global__ __launch_bounds__(kTileThreads) void k_swiglu_ck_bwd(SwigluCkArgs a) 
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         swiglu_grad_f32(i & 1 ? bf16_hi(wd[i >> 1]) : bf16_lo(wd[i >> 1]), fa[i], fb[i], ga[i], gb[i]);
-      da[j] = make_uint4(pack_bf16x2(ga[0], ga[1]), pack_bf16x2(ga[2], ga[3]), pack_bf16x2(ga[4], ga[5]),
-                         pack_bf16x2(ga[6], ga[7]));
-      db[j] = make_uint4(pack_bf16x2(gb[0], gb[1]), pack_bf16x2(gb[2], gb[3]), pack_bf16x2(gb[4], gb[5]),
-                         pack_bf16x2(gb[6], gb[7]));
+      const bool ok = (int)(threadIdx.x >> 4) + 16 * j < rows_valid && (int)(threadIdx.x & 15) * 8 < cols_valid;
+      da[j] = ok ? pack8(ga) : make_uint4(0, 0, 0, 0);
+      db[j] = ok ? pack8(gb) : make_uint4(0, 0, 0, 0);
+      // one chunk's 32 float32 values at a time: left to itself the scheduler
+      // widens all eight chunks first (256 VGPRs, 1 wave per SIMD)
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   const TileOut orow{a.q_row, a.s_row, H2, a.rows, a.k128};
