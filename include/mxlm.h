@@ -18,7 +18,8 @@
  * Column-wise codes are taken over the rows filled up with zero rows to
  * T_pad, the next multiple of the layout's step (128 for MX_SCALES_K128, 32
  * for MX_SCALES_PLAIN): q_col [cols, T_pad], s_col the scales of that matrix.
- * They are then operands of mx_scaled_mm with K = T_pad.
+ * They are then operands of mx_scaled_mm with K = T_pad. Row strides are at
+ * most 2^26 elements where nothing else is stated.
  *
  * "MX(v)" below is the quantization of mx_quantize in the call's mode and
  * layout, applied to a bf16 matrix.
@@ -78,7 +79,7 @@ mx_status mx_add_rmsnorm_bwd(const void* dy, int64_t ld_dy, const float* w,
 /* mx_swiglu_quant_fwd for any number of rows, which also keeps its input in
  * 8 bits: q_row / s_row and q_col / s_col as there (column-wise over T_pad
  * rows), q_ck [rows, 2*hidden] / s_ck = MX([a | b]) along 2*hidden.
- * hidden a multiple of 32 (128 for MX_SCALES_K128). */
+ * hidden a positive multiple of 32 (128 for MX_SCALES_K128), at most 2^25. */
 mx_status mx_swiglu_ckpt_fwd(const void* a, const void* b, int64_t ld_ab,
                              int64_t rows, int64_t hidden, mx_scale_mode mode,
                              mx_scale_layout layout, uint8_t* q_row,
@@ -130,7 +131,7 @@ mx_status mx_token_logprobs(const void* x, mx_dtype x_dtype, int64_t ld,
  * is filled up with zeros to V_pad, the next multiple of the layout's step:
  * q_row [rows, V_pad], s_row MX(G) along the vocabulary; q_col
  * [V_pad, T_pad], s_col along the rows. A row with nothing left has gradient
- * 0. */
+ * 0. vocab <= 2^26 - 128, ld <= 2^26. */
 mx_status mx_token_logprobs_bwd(const void* x, mx_dtype x_dtype, int64_t ld,
                                 int64_t rows, int64_t vocab,
                                 const int64_t* targets, int64_t ignore_index,

@@ -16,6 +16,10 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t)65535 * 128;   // one grid row per 128 tokens
 
+// The tile kernels address the 16 rows between two of a thread's chunks with
+// 32-bit byte offsets.
+constexpr int64_t kMaxStride = 1ll << 26;
+
 bool al8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 int64_t step_of(mx_scale_layout layout) { return layout == MX_SCALES_K128 ? 128 : 32; }
 int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
@@ -51,6 +55,7 @@ mx_status check_rows(const char* fn, const char* name, const void* p, int64_t ld
   MX_REQUIRE(al16(p) && ld >= cols && ld % 8 == 0, MX_ERR_ALIGN,
              "%s: %s must be 16-byte aligned with a row stride (%lld) >= the row length and a multiple of 8", fn,
              name, (long long)ld);
+  MX_REQUIRE(ld <= kMaxStride, MX_ERR_SHAPE, "%s: %s row stride (%lld) above 2^26", fn, name, (long long)ld);
   return MX_OK;
 }
 
@@ -148,7 +153,7 @@ static mx_status check_swiglu_ck(const char* fn, int64_t rows, int64_t hidden, m
                                  const uint8_t* q_col, const uint8_t* s_col, const uint8_t* q_ck,
                                  const uint8_t* s_ck) {
   MX_CHECK(check_format(fn, mode, layout));
-  MX_CHECK(check_extent(fn, rows, hidden, layout, 1ll << 30));
+  MX_CHECK(check_extent(fn, rows, hidden, layout, kMaxStride / 2));
   if (rows == 0) return MX_OK;
   MX_CHECK(check_pair(fn, "row-wise", q_row, s_row, layout, false));
   MX_CHECK(check_pair(fn, "column-wise", q_col, s_col, layout, false));
@@ -231,6 +236,7 @@ mx_status mx_token_logprobs_bwd(const void* x, mx_dtype x_dtype, int64_t ld, int
   const char* fn = "mx_token_logprobs_bwd";
   MX_CHECK(check_format(fn, mode, layout));
   MX_CHECK(check_logits(fn, x, x_dtype, ld, rows, vocab, scale));
+  MX_REQUIRE(vocab <= kMaxStride - 128 && ld <= kMaxStride, MX_ERR_SHAPE, "%s: vocab or ld above 2^26", fn);
   if (rows == 0) return MX_OK;
   MX_REQUIRE(targets && stats && entropy, MX_ERR_NULL, "%s: targets/stats/entropy NULL", fn);
   MX_REQUIRE(al8(targets) && al8(stats) && al4(entropy) && al4(dlogp) && al4(dent) && al4(dev_err), MX_ERR_ALIGN,

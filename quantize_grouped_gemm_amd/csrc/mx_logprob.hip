@@ -14,6 +14,7 @@
 // by element.
 
 #include "mx_device.h"
+#include "mx_fmt.h"
 #include "mx_lm.h"
 #include "mx_row.h"
 #include "mx_tile.h"
@@ -170,56 +171,107 @@ __global__ __launch_bounds__(256) void k_logprob_fwd(LogprobArgs a) {
 
 // ---------------------------------------------------------------- backward
 
-// In base 2: l_j = (x_j - m) c - ls log2(e), p_j = 2^l_j, and with
-//   k1 = -scale ln2 dent, k0 = -scale (dlogp + dent entropy)
-// the gradient is p_j (k1 l_j + k0), plus scale dlogp at the target. l is
-// bounded below where it multiplies k1, so that a masked entry gives p = 0
-// times a finite number; a NaN still reaches the result through p.
+// With l_j = (x_j - m) scale - ls, p_j = e^l_j and
+//   k1 = -scale dent, k0 = -scale (dlogp + dent entropy), add = scale dlogp
+// the gradient is p_j (k1 l_j + k0), plus `add` at the target. l is bounded
+// below where it multiplies k1, so that a masked entry gives p = 0 times a
+// finite number; a NaN still reaches the result through p.
+struct GradRow {
+  float m, nls, k1, k0, add;
+  int32_t target;   // column within the tile, out of [0, 128) if elsewhere
+};
+
+// Raw logits of a thread's chunks.
 template <bool F32>
+struct RawChunk {
+  uint4 w[F32 ? 2 : 1];
+};
+
+template <class F, bool F32, bool FULL>
+__device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& l, GradRow* rows, int64_t r0, int64_t c0,
+                                                 int rows_valid, int rows_pad, int cols_valid, int cols_pad) {
+  constexpr int kB = F32 ? 4 : 2;
+  const uint32_t t = threadIdx.x, cc = t & 15, tr = t >> 4;
+  const char* base = static_cast<const char*>(a.x) + (r0 * a.ld + c0) * kB;
+  RawChunk<F32> raw[kTileChunks];
+#pragma unroll
+  for (int j = 0; j < kTileChunks; ++j) {
+    if constexpr (FULL) {
+      __builtin_memcpy(&raw[j], base + (int64_t)(16 * j) * a.ld * kB + (tr * (uint32_t)a.ld + cc * 8) * kB, sizeof(raw[j]));
+    } else {
+      float f[8];
+      const int row = tr + 16 * j;
+      if (row < rows_valid && (int)cc * 8 < cols_valid)
+        load_logits<F32>(base + row * a.ld * kB, cc * 8, cols_valid, -INFINITY, f);
+      else
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = -INFINITY;
+      if constexpr (F32) __builtin_memcpy(&raw[j], f, 32);
+      else raw[j].w[0] = pack8(f);
+    }
+  }
+  if ((int)t < kTR) {
+    GradRow g{0.0f, 0.0f, 0.0f, 0.0f, 0.0f, -1};
+    if (FULL || (int)t < rows_valid) {
+      const int64_t row = r0 + t;
+      const float m = a.stats[2 * row], ls = a.stats[2 * row + 1];
+      const int64_t tg = row_target(a, row);
+      if (blockIdx.x == 0 && a.dev_err && tg < 0 && a.targets[row] != a.ignore_index) atomicOr(a.dev_err, 8);
+      if (!(m == -INFINITY && ls == -INFINITY)) {   // a row with nothing left has gradient 0
+        const float d = tg >= 0 && a.dlogp ? a.dlogp[row] : 0.0f;
+        const float dent = a.dent ? a.dent[row] : 0.0f;
+        g = GradRow{m, -ls, -a.scale * dent, -a.scale * (a.dent ? fmaf(dent, a.ent_in[row], d) : d), a.scale * d,
+                    tg >= c0 && tg < c0 + kTC ? (int32_t)(tg - c0) : -1};
+      }
+    }
+    rows[t] = g;
+  }
+  __syncthreads();
+  uint4 v[kTileChunks];
+#pragma unroll
+  for (int j = 0; j < kTileChunks; ++j) {
+    const GradRow g = rows[tr + 16 * j];
+    float f[8];
+    if constexpr (F32) __builtin_memcpy(f, &raw[j], 32);
+    else unpack8(raw[j].w[0], f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float lp = fmaf(f[k] - g.m, a.scale, g.nls);
+      const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
+      f[k] = fmaf(p, fmaf(fmaxf(lp, -1e4f), g.k1, g.k0), 0.0f);
+    }
+    const uint32_t hit = (uint32_t)g.target - cc * 8;
+    if (hit < 8) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if ((int)hit == k) f[k] += g.add;
+    }
+    v[j] = pack8(f);
+    if constexpr (!FULL) {   // rows and columns that only fill up: +0
+      const int left = (int)(tr + 16 * j) < rows_valid ? cols_valid - (int)cc * 8 : 0;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v[j]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = left >= 2 * k + 2 ? w[k] : left == 2 * k + 1 ? w[k] & 0xFFFFu : 0u;
+    }
+  }
+  fmt_dual<F, FULL>(v, l, rows_valid, rows_pad, cols_pad, TileOut{a.q_row, a.s_row, a.vocab_pad, a.rows, F::k128},
+                    TileOut{a.q_col, a.s_col, a.rows_pad, a.vocab_pad, F::k128}, r0, c0, false);
+}
+
+template <class F, bool F32>
 __global__ __launch_bounds__(kTileThreads) void k_logprob_bwd(LogprobArgs a) {
-  __shared__ uint4 lds[kTR * kTC / 8];
-  const int t = threadIdx.x, cc = t & 15;
+  __shared__ TileLds l;
+  __shared__ GradRow rows[kTR];
   const int64_t r0 = (int64_t)blockIdx.y * kTR;
   const int64_t c0 = (int64_t)blockIdx.x * kTC;
   const int rows_valid = (int)min<int64_t>(kTR, a.rows - r0);
   const int rows_pad = (int)min<int64_t>(kTR, a.rows_pad - r0);
+  const int cols_valid = (int)min<int64_t>(kTC, a.vocab - c0);
   const int cols_pad = (int)min<int64_t>(kTC, a.vocab_pad - c0);
-  const float c = a.scale * kLog2e;
-  uint4 v[kTileChunks];
-#pragma unroll
-  for (int j = 0; j < kTileChunks; ++j) {
-    const int64_t row = r0 + (t >> 4) + 16 * j;
-    const int64_t col = c0 + cc * 8;
-    v[j] = make_uint4(0, 0, 0, 0);
-    if (row < a.rows && col < a.vocab) {
-      const float m = a.stats[2 * row], ls = a.stats[2 * row + 1];
-      const int64_t tg = row_target(a, row);
-      if (blockIdx.x == 0 && cc == 0 && a.dev_err && tg < 0 && a.targets[row] != a.ignore_index)
-        atomicOr(a.dev_err, 8);
-      const float g = tg >= 0 && a.dlogp ? a.dlogp[row] : 0.0f;
-      const float dent = a.dent ? a.dent[row] : 0.0f;
-      const float l0 = -ls * kLog2e;
-      const float k1 = -a.scale * kLn2 * dent;
-      const float k0 = -a.scale * (g + (a.dent ? dent * a.ent_in[row] : 0.0f));
-      if (!(m == -INFINITY && ls == -INFINITY)) {   // a row with nothing left has gradient 0
-        float f[8];
-        load_logits<F32>(logits_row<F32>(a, row), col, a.vocab, -INFINITY, f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float l = fmaf(f[k] - m, c, l0);
-          const float p = __builtin_amdgcn_exp2f(l);
-          f[k] = fmaf(p, fmaf(fmaxf(l, -1e4f), k1, k0), 0.0f);
-          if (col + k == tg) f[k] += a.scale * g;
-          if (col + k >= a.vocab) f[k] = 0.0f;
-        }
-        v[j] = pack8(f);
-      }
-    }
-  }
-  tile_rowq(v, rows_valid, cols_pad, a.rceil, TileOut{a.q_row, a.s_row, a.vocab_pad, a.rows, a.k128}, r0, c0);
-  tile_to_lds(v, lds);
-  __syncthreads();
-  tile_colq(lds, rows_pad, cols_pad, a.rceil, TileOut{a.q_col, a.s_col, a.rows_pad, a.vocab_pad, a.k128}, r0, c0);
+  if (rows_valid == kTR && cols_valid == kTC)
+    logprob_bwd_tile<F, F32, true>(a, l, rows, r0, c0, kTR, kTR, kTC, kTC);
+  else
+    logprob_bwd_tile<F, F32, false>(a, l, rows, r0, c0, rows_valid, rows_pad, cols_valid, cols_pad);
 }
 
 // ---------------------------------------------------------------- launch
@@ -235,8 +287,10 @@ hipError_t launch_logprob_fwd(const LogprobArgs& a, hipStream_t s) {
 
 hipError_t launch_logprob_bwd(const LogprobArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.vocab_pad + kTC - 1) / kTC), (unsigned)((a.rows_pad + kTR - 1) / kTR));
-  if (a.f32) hipLaunchKernelGGL(k_logprob_bwd<true>, grid, dim3(kTileThreads), 0, s, a);
-  else hipLaunchKernelGGL(k_logprob_bwd<false>, grid, dim3(kTileThreads), 0, s, a);
+  with_fmt(a.rceil, a.k128, [&](auto f) {
+    if (a.f32) hipLaunchKernelGGL((k_logprob_bwd<decltype(f), true>), grid, dim3(kTileThreads), 0, s, a);
+    else hipLaunchKernelGGL((k_logprob_bwd<decltype(f), false>), grid, dim3(kTileThreads), 0, s, a);
+  });
   return hipGetLastError();
 }
 

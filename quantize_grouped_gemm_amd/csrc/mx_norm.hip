@@ -10,6 +10,7 @@
 // reads s or dx back in 128 x 128 tiles (mx_tile.h).
 
 #include "mx_device.h"
+#include "mx_fmt.h"
 #include "mx_lm.h"
 #include "mx_row.h"
 #include "mx_tile.h"
@@ -162,30 +163,42 @@ struct NormColArgs {
   uint8_t *q, *s;
 };
 
-template <bool NORM>
+template <class F, bool NORM, bool FULL>
+__device__ __forceinline__ void norm_col_tile(const NormColArgs& a, TileLds& l, int64_t r0, int64_t c0, int rows_valid,
+                                              int rows_pad, int cols_valid) {
+  uint4 v[kTileChunks];
+  fmt_load<FULL>(v, a.x + r0 * a.ld + c0, a.ld, rows_valid, cols_valid);
+  const int t = threadIdx.x, cc = t & 15;
+  if constexpr (NORM) {
+    float w[8] = {};
+    if (FULL || cc * 8 < cols_valid) load8f(a.w + c0 + cc * 8, w);
+#pragma unroll
+    for (int j = 0; j < kTileChunks; ++j) {
+      const int row = (t >> 4) + 16 * j;
+      // rows past the last stay +0 whatever w holds
+      if (FULL || row < rows_valid) v[j] = norm_chunk(v[j], a.rstd[r0 + row], w);
+    }
+  }
+  fmt_to_lds(v, l);
+  __syncthreads();
+  const TileOut o{a.q, a.s, a.rows_pad, a.cols, F::k128};
+  fmt_colq<F, FULL>(l, rows_pad, cols_valid, o, r0, c0);
+  __syncthreads();
+  if (t < kTC) fmt_scales<F>(l.s_col, t, cols_valid, rows_pad, o, c0, r0);
+}
+
+template <class F, bool NORM>
 __global__ __launch_bounds__(kTileThreads) void k_norm_col(NormColArgs a) {
-  __shared__ uint4 lds[kTR * kTC / 8];
+  __shared__ TileLds l;
   const int64_t r0 = (int64_t)blockIdx.y * kTR;
   const int64_t c0 = (int64_t)blockIdx.x * kTC;
   const int rows_valid = (int)min<int64_t>(kTR, a.rows - r0);
   const int rows_pad = (int)min<int64_t>(kTR, a.rows_pad - r0);
   const int cols_valid = (int)min<int64_t>(kTC, a.cols - c0);
-  uint4 v[kTileChunks];
-  tile_load(v, a.x + r0 * a.ld + c0, a.ld, rows_valid, cols_valid);
-  if constexpr (NORM) {
-    const int t = threadIdx.x, cc = t & 15;
-    float w[8] = {};
-    if (cc * 8 < cols_valid) load8f(a.w + c0 + cc * 8, w);
-#pragma unroll
-    for (int j = 0; j < kTileChunks; ++j) {
-      const int row = (t >> 4) + 16 * j;
-      // rows past the last stay +0 whatever w holds
-      if (row < rows_valid) v[j] = norm_chunk(v[j], a.rstd[r0 + row], w);
-    }
-  }
-  tile_to_lds(v, lds);
-  __syncthreads();
-  tile_colq(lds, rows_pad, cols_valid, a.rceil, TileOut{a.q, a.s, a.rows_pad, a.cols, a.k128}, r0, c0);
+  if (rows_valid == kTR && cols_valid == kTC)
+    norm_col_tile<F, NORM, true>(a, l, r0, c0, kTR, kTR, kTC);
+  else
+    norm_col_tile<F, NORM, false>(a, l, r0, c0, rows_valid, rows_pad, cols_valid);
 }
 
 // ---------------------------------------------------------------- launch
@@ -211,7 +224,9 @@ static void with_row_shape(int64_t cols, F f) {
 template <bool NORM>
 static void launch_col(const NormColArgs& c, hipStream_t s) {
   const dim3 grid((unsigned)((c.cols + kTC - 1) / kTC), (unsigned)((c.rows_pad + kTR - 1) / kTR));
-  hipLaunchKernelGGL(k_norm_col<NORM>, grid, dim3(kTileThreads), 0, s, c);
+  with_fmt(c.rceil, c.k128, [&](auto f) {
+    hipLaunchKernelGGL((k_norm_col<decltype(f), NORM>), grid, dim3(kTileThreads), 0, s, c);
+  });
 }
 
 hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t s) {

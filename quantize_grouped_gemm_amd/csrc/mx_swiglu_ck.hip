@@ -4,39 +4,51 @@
 //                     along its rows (the checkpoint)
 //   k_swiglu_ck_bwd   a, b from the checkpoint; [dA | dB] quantized both ways
 //
-// One 128 x 128 tile of h per workgroup in the tile scheme of mx_tile.h: each
+// One 128 x 128 tile of h per workgroup in the tile scheme of mx_tile.h and mx_fmt.h: each
 // input is read once into registers, everything else happens on chip. Rows
 // past the last one enter as zeros, so the column-wise blocks that they fill
 // up quantize to zeros.
 
 #include "mx_device.h"
+#include "mx_fmt.h"
 #include "mx_lm.h"
 #include "mx_row.h"
 #include "mx_tile.h"
 
 namespace mxk {
 
+template <class F, bool FULL>
+__device__ __forceinline__ void swiglu_ck_fwd_tile(const SwigluCkArgs& a, TileLds& l, uint32_t (&s_ck)[2][kTR], int64_t r0,
+                                                   int64_t c0, int rows_valid, int rows_pad, int cols_valid) {
+  uint4 v[kTileChunks], w[kTileChunks];
+  fmt_load<FULL>(v, a.a + r0 * a.ld_ab + c0, a.ld_ab, rows_valid, cols_valid);
+  fmt_load<FULL>(w, a.b + r0 * a.ld_ab + c0, a.ld_ab, rows_valid, cols_valid);
+  const TileOut ock{a.q_ck, a.s_ck, 2 * a.hidden, a.rows, F::k128};
+  fmt_rowq<F, FULL>(v, rows_valid, cols_valid, ock, r0, c0, s_ck[0]);
+  fmt_rowq<F, FULL>(w, rows_valid, cols_valid, ock, r0, a.hidden + c0, s_ck[1]);
+#pragma unroll
+  for (int j = 0; j < kTileChunks; ++j)
+    v[j] = make_uint4(swiglu_pair(v[j].x, w[j].x), swiglu_pair(v[j].y, w[j].y),
+                      swiglu_pair(v[j].z, w[j].z), swiglu_pair(v[j].w, w[j].w));
+  fmt_dual<F, FULL>(v, l, rows_valid, rows_pad, cols_valid, TileOut{a.q_row, a.s_row, a.hidden, a.rows, F::k128},
+                    TileOut{a.q_col, a.s_col, a.rows_pad, a.hidden, F::k128}, r0, c0, false);
+  const int t = threadIdx.x & (kTR - 1), half = threadIdx.x / kTR;
+  fmt_scales<F>(s_ck[half], t, rows_valid, cols_valid, ock, r0, half * a.hidden + c0);
+}
+
+template <class F>
 __global__ __launch_bounds__(kTileThreads) void k_swiglu_ck_fwd(SwigluCkArgs a) {
-  __shared__ uint4 lds[kTR * kTC / 8];
+  __shared__ TileLds l;
+  __shared__ uint32_t s_ck[2][kTR];
   const int64_t r0 = (int64_t)blockIdx.y * kTR;
   const int64_t c0 = (int64_t)blockIdx.x * kTC;
   const int rows_valid = (int)min<int64_t>(kTR, a.rows - r0);
   const int rows_pad = (int)min<int64_t>(kTR, a.rows_pad - r0);
   const int cols_valid = (int)min<int64_t>(kTC, a.hidden - c0);
-  uint4 v[kTileChunks], w[kTileChunks];
-  tile_load<true>(v, a.a + r0 * a.ld_ab + c0, a.ld_ab, rows_valid, cols_valid);
-  tile_load<true>(w, a.b + r0 * a.ld_ab + c0, a.ld_ab, rows_valid, cols_valid);
-  const TileOut ock{a.q_ck, a.s_ck, 2 * a.hidden, a.rows, a.k128};
-  tile_rowq(v, rows_valid, cols_valid, a.rceil, ock, r0, c0);
-  tile_rowq(w, rows_valid, cols_valid, a.rceil, ock, r0, a.hidden + c0);
-#pragma unroll
-  for (int j = 0; j < kTileChunks; ++j)
-    v[j] = make_uint4(swiglu_pair(v[j].x, w[j].x), swiglu_pair(v[j].y, w[j].y),
-                      swiglu_pair(v[j].z, w[j].z), swiglu_pair(v[j].w, w[j].w));
-  tile_rowq(v, rows_valid, cols_valid, a.rceil, TileOut{a.q_row, a.s_row, a.hidden, a.rows, a.k128}, r0, c0);
-  tile_to_lds(v, lds);
-  __syncthreads();
-  tile_colq(lds, rows_pad, cols_valid, a.rceil, TileOut{a.q_col, a.s_col, a.rows_pad, a.hidden, a.k128}, r0, c0);
+  if (rows_valid == kTR && cols_valid == kTC)
+    swiglu_ck_fwd_tile<F, true>(a, l, s_ck, r0, c0, kTR, kTR, kTC);
+  else
+    swiglu_ck_fwd_tile<F, false>(a, l, s_ck, r0, c0, rows_valid, rows_pad, cols_valid);
 }
 
 // Codes and scale bytes of the thread's chunks of a tile whose (0,0) is row
@@ -44,36 +56,44 @@ __global__ __launch_bounds__(kTileThreads) void k_swiglu_ck_fwd(SwigluCkArgs a) 
 // read its last row or column in their place (loads without a branch: with
 // one, the compiler carried the widened float32 values of all chunks through
 // it, 256 VGPRs); the caller drops what comes of them.
+template <class F, bool FULL>
 __device__ __forceinline__ void tile_load_codes(uint2 (&q)[kTileChunks], uint32_t (&sb)[kTileChunks], const uint8_t* qp,
-                                                const uint8_t* sp, int64_t ld, int64_t rows, bool k128, int64_t r0,
-                                                int64_t c0, int rows_valid, int cols_valid) {
-  const int t = threadIdx.x;
-  const int64_t c = c0 + min((t & 15) * 8, cols_valid - 8);
+                                                const uint8_t* sp, int64_t ld, int64_t rows, int64_t r0, int64_t c0,
+                                                int rows_valid, int cols_valid) {
+  const uint32_t t = threadIdx.x;
+  const uint32_t c = FULL ? (t & 15) * 8 : (uint32_t)min((int)(t & 15) * 8, cols_valid - 8);
+  const uint8_t* qbase = qp + r0 * ld + c0;
+  const uint8_t* sbase = sp + (F::k128 ? ((c0 >> 7) * rows + r0) * 4 : r0 * (ld / kBlock) + (c0 >> 5));
+  const uint32_t sld = F::k128 ? 4u : (uint32_t)(ld / kBlock);
 #pragma unroll
   for (int j = 0; j < kTileChunks; ++j) {
-    const int64_t r = r0 + min((t >> 4) + 16 * j, rows_valid - 1);
-    q[j] = *reinterpret_cast<const uint2*>(qp + r * ld + c);
-    sb[j] = sp[k128 ? ((c >> 7) * rows + r) * 4 + ((c >> 5) & 3) : r * (ld / kBlock) + (c >> 5)];
+    const uint32_t r = FULL ? (t >> 4) + 16 * j : (uint32_t)min((int)(t >> 4) + 16 * j, rows_valid - 1);
+    if constexpr (FULL) {
+      q[j] = *reinterpret_cast<const uint2*>(qbase + (int64_t)(16 * j) * ld + ((t >> 4) * (uint32_t)ld + c));
+      sb[j] = sbase[(int64_t)(16 * j) * sld + ((t >> 4) * sld + (c >> 5))];
+    } else {
+      q[j] = *reinterpret_cast<const uint2*>(qbase + r * ld + c);
+      sb[j] = sbase[(int64_t)r * sld + (c >> 5)];
+    }
   }
 }
 
-__global__ __launch_bounds__(kTileThreads, 4) void k_swiglu_ck_bwd(SwigluCkArgs a) {
-  __shared__ uint4 lds[kTR * kTC / 8];
-  const int64_t r0 = (int64_t)blockIdx.y * kTR;
-  const int64_t c0 = (int64_t)blockIdx.x * kTC;
-  const int rows_valid = (int)min<int64_t>(kTR, a.rows - r0);
-  const int rows_pad = (int)min<int64_t>(kTR, a.rows_pad - r0);
-  const int cols_valid = (int)min<int64_t>(kTC, a.hidden - c0);
+template <class F, bool FULL>
+__device__ __forceinline__ void swiglu_ck_bwd_tile(const SwigluCkArgs& a, TileLds& l, int64_t r0, int64_t c0,
+                                                   int rows_valid, int rows_pad, int cols_valid) {
   const int64_t H2 = 2 * a.hidden;
   uint4 da[kTileChunks], db[kTileChunks];
   {
     uint2 qa[kTileChunks], qb[kTileChunks];
     uint32_t sa[kTileChunks], sb[kTileChunks];
-    tile_load<true>(da, a.dh + r0 * a.ld_dh + c0, a.ld_dh, rows_valid, cols_valid);
-    tile_load_codes(qa, sa, a.q_ck, a.s_ck, H2, a.rows, a.k128, r0, c0, rows_valid, cols_valid);
-    tile_load_codes(qb, sb, a.q_ck, a.s_ck, H2, a.rows, a.k128, r0, a.hidden + c0, rows_valid, cols_valid);
+    fmt_load<FULL>(da, a.dh + r0 * a.ld_dh + c0, a.ld_dh, rows_valid, cols_valid);
+    tile_load_codes<F, FULL>(qa, sa, a.q_ck, a.s_ck, H2, a.rows, r0, c0, rows_valid, cols_valid);
+    tile_load_codes<F, FULL>(qb, sb, a.q_ck, a.s_ck, H2, a.rows, r0, a.hidden + c0, rows_valid, cols_valid);
 #pragma unroll
     for (int j = 0; j < kTileChunks; ++j) {
+      // one chunk's 32 float32 values at a time: left to itself the compiler
+      // widens all eight chunks first
+      asm volatile("" : "+v"(qa[j].x), "+v"(qa[j].y), "+v"(qb[j].x), "+v"(qb[j].y));
       float fa[8], fb[8], ga[8], gb[8];
       e4m3_chunk_values(qa[j], sa[j], fa);
       e4m3_chunk_values(qb[j], sb[j], fb);
@@ -81,25 +101,31 @@ __global__ __launch_bounds__(kTileThreads, 4) void k_swiglu_ck_bwd(SwigluCkArgs 
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         swiglu_grad_f32(i & 1 ? bf16_hi(wd[i >> 1]) : bf16_lo(wd[i >> 1]), fa[i], fb[i], ga[i], gb[i]);
-      const bool ok = (int)(threadIdx.x >> 4) + 16 * j < rows_valid && (int)(threadIdx.x & 15) * 8 < cols_valid;
+      const bool ok = FULL || ((int)(threadIdx.x >> 4) + 16 * j < rows_valid && (int)(threadIdx.x & 15) * 8 < cols_valid);
       da[j] = ok ? pack8(ga) : make_uint4(0, 0, 0, 0);
       db[j] = ok ? pack8(gb) : make_uint4(0, 0, 0, 0);
-      // one chunk's 32 float32 values at a time: left to itself the scheduler
-      // widens all eight chunks first (256 VGPRs, 1 wave per SIMD)
-      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" : "+v"(da[j].x), "+v"(da[j].y), "+v"(da[j].z), "+v"(da[j].w), "+v"(db[j].x), "+v"(db[j].y),
+                        "+v"(db[j].z), "+v"(db[j].w));
     }
   }
-  const TileOut orow{a.q_row, a.s_row, H2, a.rows, a.k128};
-  tile_rowq(da, rows_valid, cols_valid, a.rceil, orow, r0, c0);
-  tile_rowq(db, rows_valid, cols_valid, a.rceil, orow, r0, a.hidden + c0);
-  const TileOut ocol{a.q_col, a.s_col, a.rows_pad, H2, a.k128};
-  tile_to_lds(da, lds);
-  __syncthreads();
-  tile_colq(lds, rows_pad, cols_valid, a.rceil, ocol, r0, c0);
-  __syncthreads();
-  tile_to_lds(db, lds);
-  __syncthreads();
-  tile_colq(lds, rows_pad, cols_valid, a.rceil, ocol, r0, a.hidden + c0);
+  const TileOut orow{a.q_row, a.s_row, H2, a.rows, F::k128};
+  const TileOut ocol{a.q_col, a.s_col, a.rows_pad, H2, F::k128};
+  fmt_dual<F, FULL>(da, l, rows_valid, rows_pad, cols_valid, orow, ocol, r0, c0, true);
+  fmt_dual<F, FULL>(db, l, rows_valid, rows_pad, cols_valid, orow, ocol, r0, a.hidden + c0, false);
+}
+
+template <class F>
+__global__ __launch_bounds__(kTileThreads, 4) void k_swiglu_ck_bwd(SwigluCkArgs a) {
+  __shared__ TileLds l;
+  const int64_t r0 = (int64_t)blockIdx.y * kTR;
+  const int64_t c0 = (int64_t)blockIdx.x * kTC;
+  const int rows_valid = (int)min<int64_t>(kTR, a.rows - r0);
+  const int rows_pad = (int)min<int64_t>(kTR, a.rows_pad - r0);
+  const int cols_valid = (int)min<int64_t>(kTC, a.hidden - c0);
+  if (rows_valid == kTR && cols_valid == kTC)
+    swiglu_ck_bwd_tile<F, true>(a, l, r0, c0, kTR, kTR, kTC);
+  else
+    swiglu_ck_bwd_tile<F, false>(a, l, r0, c0, rows_valid, rows_pad, cols_valid);
 }
 
 static dim3 tile_grid(const SwigluCkArgs& a) {
@@ -107,12 +133,16 @@ static dim3 tile_grid(const SwigluCkArgs& a) {
 }
 
 hipError_t launch_swiglu_ck_fwd(const SwigluCkArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(k_swiglu_ck_fwd, tile_grid(a), dim3(kTileThreads), 0, s, a);
+  with_fmt(a.rceil, a.k128, [&](auto f) {
+    hipLaunchKernelGGL(k_swiglu_ck_fwd<decltype(f)>, tile_grid(a), dim3(kTileThreads), 0, s, a);
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_swiglu_ck_bwd(const SwigluCkArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(k_swiglu_ck_bwd, tile_grid(a), dim3(kTileThreads), 0, s, a);
+  with_fmt(a.rceil, a.k128, [&](auto f) {
+    hipLaunchKernelGGL(k_swiglu_ck_bwd<decltype(f)>, tile_grid(a), dim3(kTileThreads), 0, s, a);
+  });
   return hipGetLastError();
 }
 
