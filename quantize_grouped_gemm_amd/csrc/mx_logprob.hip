@@ -1,13 +1,13 @@
 // Log probabilities of given tokens, with entropy and top alternatives, and
 // the gradient of the logits as an MX operand:
-//   k_logprob_fwd   one workgroup per row
-//   k_logprob_bwd   one 128 x 128 tile per workgroup (mx_tile.h)
+//   k_logprob_part   sums, maximum and best entries of a row or of a segment
+//   k_logprob_join   joins the segments of a row
+//   k_logprob_bwd    one 128 x 128 tile of the gradient per workgroup
 //
 // In base 2: with c = scale log2(e) and d_j = (x_j - m) c, the row's sums are
-// S = sum 2^d_j and A = sum 2^d_j d_j, kept relative to a running maximum m
-// (a new maximum m' multiplies S by f = 2^((m - m') c) and turns A into
-// f (A + S (m - m') c)); then ls = ln S, entropy = ln S - ln2 A / S. Nothing
-// overflows and a masked entry (-infinity) adds exactly 0.
+// S = sum 2^d_j and A = sum 2^d_j d_j, m the row's maximum; then ls = ln S,
+// entropy = ln S - ln2 A / S. Nothing overflows and a masked entry
+// (-infinity) adds exactly 0.
 //
 // Rows may start at any element (an odd vocabulary), so chunks are read with
 // 16-byte loads of 2- or 4-byte alignment and the last one of a row element
@@ -21,6 +21,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace mxk {
 
@@ -63,9 +64,9 @@ __device__ __forceinline__ int64_t row_target(const LogprobArgs& a, int64_t row)
 }
 
 // Order of the alternatives as one number: larger for a larger value, then
-// for a lower index (the sign of zero does not count).
+// for a lower index (the sign of zero does not count, a NaN comes first).
 __device__ __forceinline__ uint64_t top_key(float x, uint32_t idx) {
-  const uint32_t u = __float_as_uint(x + 0.0f);
+  const uint32_t u = x == x ? __float_as_uint(x + 0.0f) : 0x7FC00000u;
   const uint32_t o = u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
   return ((uint64_t)o << 32) | (0xFFFFFFFFu - idx);
 }
@@ -100,41 +101,195 @@ __device__ __forceinline__ Soft soft_join(Soft u, Soft v, float c) {
   return Soft{m, u.s + v.s, u.a + v.a};
 }
 
+// Raw logits of a thread's chunks.
 template <bool F32>
-__global__ __launch_bounds__(256) void k_logprob_fwd(LogprobArgs a) {
-  __shared__ Soft part[4];
-  __shared__ uint64_t best[4];
-  const int t = threadIdx.x;
-  const int64_t row = blockIdx.x;
-  const void* x = logits_row<F32>(a, row);
-  const float c = a.scale * kLog2e;
-  Soft v{-INFINITY, 0.0f, 0.0f};
-  for (int64_t i = 8 * (int64_t)t; i < a.vocab; i += 8 * 256) {
-    float f[8];
-    load_logits<F32>(x, i, a.vocab, -INFINITY, f);
-    float m = v.m;
+struct RawChunk {
+  uint4 w[F32 ? 2 : 1];
+};
+
+// ---------------------------------------------------------------- forward
+//
+// One read of the logits. A workgroup streams its segment in tiles of
+// 256 x U chunks of 8; while it sums, each thread keeps the maximum of every
+// *slot* of its share (a slot: the thread's chunks of one or a few tiles) in
+// LDS, at the cost of the maximum that the softmax needs anyway. The `top`
+// best entries then follow from the slots: the top-th largest of the 256
+// threads' maxima is a lower bound of the top-th largest entry, so only slots
+// that reach it can hold one (about `top` of some 4096), and only those are
+// read again, from cache.
+//
+// Softmax sums are kept per thread relative to an integer r: 2^(x c - r) with
+// r = rint(c times the thread's maximum so far), raised only when a tile
+// passes it by 2^32. One fused multiply-add forms the exponent, changes of r
+// are exact powers of two, and no per-element maximum is needed.
+
+constexpr int kThreads = 256;
+constexpr int kSlots = 16;
+constexpr int kRound = 4 * kThreads;        // entries looked at between two checks of the candidate count
+constexpr int kCand = kRound + kMaxTop;
+constexpr int kList = 512;                  // slots worth reading one by one
+constexpr float kNoRef = -1e30f;
+constexpr float kFarExp = 1e29f;            // |m c| up to here suits the fast sums
+
+template <bool F32>
+constexpr int kUnroll = F32 ? 2 : 4;
+
+__device__ __forceinline__ uint32_t key16(float x) { return (uint32_t)(top_key(x, 0) >> 48); }
+
+template <int N>
+__device__ __forceinline__ float max_of(const float (&f)[N], float m) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = fmaxf(m, f[k]);
-    v = soft_rebase(v, m, c);
-    const float base = m == -INFINITY ? 0.0f : m;   // -inf - 0 keeps e = 0
+  for (int k = 0; k < N; ++k) m = fmaxf(m, f[k]);
+  return m;
+}
+
+struct TopLds {
+  uint16_t slot[kSlots][kThreads];
+  uint64_t cand[kCand];
+  uint64_t thr;          // entries with a larger key are candidates
+  uint16_t list[kList];
+  int count, hits;
+};
+
+// Keeps the `top` largest of l.cand[0 .. count), in descending order, and
+// raises the threshold to the last of them once there are `top`. Keys are
+// unique, so an entry's rank is the number of larger ones. All threads call
+// it; barriers inside, the last one after the writes.
+__device__ __forceinline__ void keep_top(TopLds& l, int top) {
+  constexpr int kPer = (kCand + kThreads - 1) / kThreads;
+  const int t = threadIdx.x;
+  __syncthreads();
+  const int n = l.count;
+  uint64_t key[kPer];
+  int rank[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int at = t + kThreads * i;
+    rank[i] = top;
+    if (at < n) {
+      key[i] = l.cand[at];
+      int r = 0;
+      for (int j = 0; j < n; ++j) r += l.cand[j] > key[i] ? 1 : 0;
+      rank[i] = r;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (rank[i] < top) {
+      l.cand[rank[i]] = key[i];
+      if (rank[i] == top - 1) l.thr = key[i];
+    }
+  }
+  if (t == 0) l.count = min(n, top);
+  __syncthreads();
+}
+
+// Offers up to 4 entries per thread; all threads call it.
+template <bool F32>
+__device__ __forceinline__ void offer(TopLds& l, const void* x, int64_t i, int64_t n, bool on, uint32_t idx0, int top) {
+  const uint64_t thr = l.thr;
+  if (on) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i + k < n) {
+        const float f = F32 ? static_cast<const float*>(x)[i + k]
+                            : __uint_as_float((uint32_t)static_cast<const uint16_t*>(x)[i + k] << 16);
+        const uint64_t key = top_key(f, idx0 + (uint32_t)(i + k));
+        if (key > thr) l.cand[atomicAdd(&l.count, 1)] = key;
+      }
+    }
+  }
+  __syncthreads();
+  const bool full = l.count > kCand - kRound;   // the next round might not fit
+  if (full) keep_top(l, top);
+  else __syncthreads();
+}
+
+// The `top` best entries of the segment [0, n) of x (first index idx0), in
+// descending order in l.cand[0 .. l.count). `slots` slots of `tiles` tiles
+// each; tmax the thread's maximum.
+template <bool F32>
+__device__ __forceinline__ void find_top(TopLds& l, const void* x, int64_t n, uint32_t idx0, float tmax, int slots,
+                                         int tiles, int top) {
+  constexpr int U = kUnroll<F32>;
+  const int t = threadIdx.x;
+  __shared__ uint16_t tkey[kThreads];
+  tkey[t] = (uint16_t)key16(tmax);
+  if (t == 0) l.count = l.hits = 0;
+  __syncthreads();
+  if (t < 64) {
+    // the top-th largest of the 256 keys, bit by bit
+    uint32_t k[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) k[i] = tkey[t + 64 * i];
+    uint32_t bound = 0;
+    for (int b = 15; b >= 0; --b) {
+      const uint32_t tryb = bound | (1u << b);
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c += __popcll(__ballot(k[i] >= tryb));
+      if (c >= top) bound = tryb;
+    }
+    if (t == 0) l.thr = bound ? ((uint64_t)bound << 48) - 1 : 0;
+  }
+  __syncthreads();
+  const uint32_t bound = (uint32_t)((l.thr + 1) >> 48);
+  for (int s = 0; s < slots; ++s) {
+    if (l.slot[s][t] >= bound) {
+      const int at = atomicAdd(&l.hits, 1);
+      if (at < kList) l.list[at] = (uint16_t)(s * kThreads + t);
+    }
+  }
+  __syncthreads();
+  const int hits = l.hits;
+  const int per = 2 * U * tiles;    // half chunks of a slot
+  if (hits <= kList) {
+    for (int base = 0; base < hits * per; base += kThreads) {
+      const int item = base + t;
+      const bool on = item < hits * per;
+      const int e = on ? l.list[item / per] : 0, h = item % per;
+      const int64_t chunk = ((int64_t)(e / kThreads) * tiles * U + (h >> 1)) * kThreads + e % kThreads;
+      offer<F32>(l, x, 8 * chunk + 4 * (h & 1), n, on, idx0, top);
+    }
+  } else {
+    // so many slots qualify (equal or sorted entries): read the segment again
+    for (int64_t base = 0; base < n; base += kRound) offer<F32>(l, x, base + 4 * t, n, true, idx0, top);
+  }
+  keep_top(l, top);
+}
+
+// S and A of the segment relative to its maximum m, by the definition; for
+// maxima whose exponents the fast sums cannot hold.
+template <bool F32>
+__device__ __forceinline__ Soft far_sums(const void* x, int64_t n, float m, float c) {
+  Soft v{m, 0.0f, 0.0f};
+  for (int64_t i = 8 * (int64_t)threadIdx.x; i < n; i += 8 * kThreads) {
+    float f[8];
+    load_logits<F32>(x, i, n, -INFINITY, f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float d = (f[k] - base) * c;
+      const float d = (f[k] - m) * c;
       const float e = __builtin_amdgcn_exp2f(d);
       v.s += e;
       v.a = fmaf(e, fmaxf(d, -1e4f), v.a);
     }
   }
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1)
-    v = soft_join(v, Soft{__shfl_xor(v.m, o), __shfl_xor(v.s, o), __shfl_xor(v.a, o)}, c);
-  if ((t & 63) == 0) part[t >> 6] = v;
-  __syncthreads();
-  v = part[0];
-  for (int i = 1; i < 4; ++i) v = soft_join(v, part[i], c);
+  return v;
+}
+
+// What a row's (joined) sums give.
+struct RowOut {
+  float m, ls;
+  bool empty;
+};
+
+template <bool F32>
+__device__ __forceinline__ RowOut store_row(const LogprobArgs& a, int64_t row, Soft v) {
   const bool empty = v.m == -INFINITY && v.s == 0.0f;
   const float ls = empty ? -INFINITY : logf(v.s);
-  if (t == 0) {
+  if (threadIdx.x == 0) {
+    const void* x = logits_row<F32>(a, row);
     const int64_t tg = row_target(a, row);
     if (a.dev_err && tg < 0 && a.targets[row] != a.ignore_index) atomicOr(a.dev_err, 8);
     float xt = 0.0f;
@@ -146,26 +301,212 @@ __global__ __launch_bounds__(256) void k_logprob_fwd(LogprobArgs a) {
     a.stats_out[2 * row] = v.m;
     a.stats_out[2 * row + 1] = ls;
   }
-  uint64_t last = ~0ull;
-  for (int j = 0; j < a.top; ++j) {
-    uint64_t b = 0;
-    for (int64_t i = 8 * (int64_t)t; i < a.vocab; i += 8 * 256) {
-      float f[8];
-      load_logits<F32>(x, i, a.vocab, -INFINITY, f);
-      for (int k = 0; k < 8; ++k) {
-        const uint64_t key = top_key(f[k], (uint32_t)(i + k));
-        if (i + k < a.vocab && key < last && key > b) b = key;
+  return RowOut{v.m, ls, empty};
+}
+
+__device__ __forceinline__ void store_top(const LogprobArgs& a, int64_t row, const uint64_t* sorted, RowOut o) {
+  const int t = threadIdx.x;
+  if (t < a.top) {
+    const uint64_t key = sorted[t];
+    a.top_idx[row * a.top + t] = (int32_t)key_index(key);
+    a.top_logp[row * a.top + t] = o.empty ? -INFINITY : (key_value(key) - o.m) * a.scale - o.ls;
+  }
+}
+
+// A row's segments: `parts` of `seg` logits each (the last one shorter).
+struct Split {
+  int32_t parts;
+  int64_t seg;
+};
+
+// Workspace of a split row: parts Softs, then (16-byte aligned) parts x top
+// keys, 0 where a segment has fewer entries.
+struct PartWork {
+  Soft* soft;
+  uint64_t* keys;
+};
+
+__host__ __device__ inline int64_t soft_bytes(int64_t rows, int64_t parts) {
+  return (rows * parts * (int64_t)sizeof(Soft) + 15) / 16 * 16;
+}
+
+__device__ __forceinline__ PartWork part_work(const LogprobArgs& a, const Split& sp) {
+  char* w = static_cast<char*>(a.work);
+  return PartWork{reinterpret_cast<Soft*>(w), reinterpret_cast<uint64_t*>(w + soft_bytes(a.rows, sp.parts))};
+}
+
+template <bool F32, bool TOP>
+__global__ __launch_bounds__(kThreads) void k_logprob_part(LogprobArgs a, Split sp) {
+  constexpr int U = kUnroll<F32>;
+  constexpr int kTile = 8 * U * kThreads;
+  __shared__ float red[3][4];
+  __shared__ std::conditional_t<TOP, TopLds, int> l;
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x / (unsigned)sp.parts;
+  const int64_t part = blockIdx.x - row * sp.parts;
+  const int64_t first = part * sp.seg;
+  const int64_t n = min(sp.seg, a.vocab - first);
+  const char* x = static_cast<const char*>(logits_row<F32>(a, row)) + first * (F32 ? 4 : 2);
+  const float c = a.scale * kLog2e;
+  const int tiles = (int)((n + kTile - 1) / kTile);
+  const int per_slot = (tiles + kSlots - 1) / kSlots;
+
+  float ref = kNoRef, s = 0.0f, A = 0.0f, tmax = -INFINITY, smax = -INFINITY;
+  RawChunk<F32> cur[U], nxt[U];
+  auto fetch = [&](int tile, RawChunk<F32> (&r)[U]) {
+    const int64_t base = (int64_t)tile * kTile;
+    if (base + kTile <= n) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        __builtin_memcpy(&r[u], x + (base + 8 * kThreads * u) * (F32 ? 4 : 2) + 8 * t * (F32 ? 4 : 2), sizeof(r[u]));
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float f[8];
+        const int64_t i = base + 8 * (kThreads * u + t);
+        if (i < n) load_logits<F32>(x, i, n, -INFINITY, f);
+        else
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = -INFINITY;
+        if constexpr (F32) __builtin_memcpy(&r[u], f, 32);
+        else r[u].w[0] = pack8(f);
       }
     }
-    for (int o = 32; o >= 1; o >>= 1) b = max(b, (uint64_t)__shfl_xor((unsigned long long)b, o));
-    __syncthreads();
-    if ((t & 63) == 0) best[t >> 6] = b;
-    __syncthreads();
-    last = max(max(best[0], best[1]), max(best[2], best[3]));
-    if (t == 0) {
-      a.top_idx[row * a.top + j] = (int32_t)key_index(last);
-      a.top_logp[row * a.top + j] = empty ? -INFINITY : (key_value(last) - v.m) * a.scale - ls;
+  };
+  fetch(0, cur);
+  int slot = 0, left = per_slot;
+  for (int tile = 0; tile < tiles; ++tile) {
+    if (tile + 1 < tiles) fetch(tile + 1, nxt);
+    float f[U][8];
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (F32) __builtin_memcpy(f[u], &cur[u], 32);
+      else unpack8(cur[u].w[0], f[u]);
+      m = max_of(f[u], m);
     }
+    if (m * c > ref + 32.0f) {
+      const float r = __builtin_rintf(m * c);
+      const float d = ref - r;
+      const float g = __builtin_amdgcn_exp2f(d);
+      A = (A + s * d) * g;
+      s *= g;
+      ref = r;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float d = fmaf(f[u][k], c, -ref);
+        const float e = __builtin_amdgcn_exp2f(d);
+        s += e;
+        A = fmaf(e, fmaxf(d, -1e4f), A);
+      }
+    smax = fmaxf(smax, m);
+    if (--left == 0 || tile + 1 == tiles) {
+      tmax = fmaxf(tmax, smax);
+      if constexpr (TOP) l.slot[slot][t] = (uint16_t)key16(smax);
+      smax = -INFINITY;
+      left = per_slot;
+      ++slot;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) cur[u] = nxt[u];
+  }
+
+  float M = tmax;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
+  if ((t & 63) == 0) red[0][t >> 6] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  Soft v;
+  if (M != -INFINITY && !(fabsf(M) * c <= kFarExp)) {
+    v = far_sums<F32>(x, n, M, c);
+  } else {
+    // relative to M itself: r - M c, then the factor 2^(r - M c)
+    const float base = M == -INFINITY ? 0.0f : M;
+    const float d = fmaf(-base, c, ref);
+    const float g = __builtin_amdgcn_exp2f(d);
+    v = Soft{M, s * g, (A + s * d) * g};
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    v.s += __shfl_xor(v.s, o);
+    v.a += __shfl_xor(v.a, o);
+  }
+  if ((t & 63) == 0) {
+    red[1][t >> 6] = v.s;
+    red[2][t >> 6] = v.a;
+  }
+  __syncthreads();
+  v.s = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  v.a = (red[2][0] + red[2][1]) + (red[2][2] + red[2][3]);
+
+  if constexpr (TOP) find_top<F32>(l, x, n, (uint32_t)first, tmax, slot, per_slot, a.top);
+  if (sp.parts == 1) {
+    const RowOut o = store_row<F32>(a, row, v);
+    if constexpr (TOP) store_top(a, row, l.cand, o);
+  } else {
+    const PartWork w = part_work(a, sp);
+    if (t == 0) w.soft[row * sp.parts + part] = v;
+    if constexpr (TOP) {
+      if (t < a.top) w.keys[(row * sp.parts + part) * a.top + t] = t < l.count ? l.cand[t] : 0;
+    }
+  }
+}
+
+constexpr int kMaxParts = 32;
+
+// One workgroup per row. The alternatives: the top-th largest of the lists'
+// first entries (`lead` of each, at least `top` in all) bounds the result from
+// below; what reaches it, rarely many more than `top`, is ranked.
+template <bool F32, bool TOP>
+__global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobArgs a, Split sp) {
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const PartWork w = part_work(a, sp);
+  const float c = a.scale * kLog2e;
+  const Soft* parts = w.soft + row * sp.parts;
+  Soft v = parts[0];
+  for (int i = 1; i < sp.parts; ++i) v = soft_join(v, parts[i], c);
+  const RowOut o = store_row<F32>(a, row, v);
+  if constexpr (TOP) {
+    __shared__ uint64_t keys[kMaxParts * kMaxTop], lead_keys[kThreads], best[kMaxTop];
+    __shared__ uint64_t bound;
+    __shared__ int count;
+    const int total = sp.parts * a.top;
+    const uint64_t* src = w.keys + row * total;
+    const int lead = min((2 * a.top + sp.parts - 1) / sp.parts, a.top);
+    const int leads = lead * sp.parts;   // at most 2 top + parts
+    if (t < leads) lead_keys[t] = src[(t / lead) * a.top + t % lead];
+    if (t == 0) {
+      bound = 1;
+      count = 0;
+    }
+    __syncthreads();
+    if (t < leads) {
+      const uint64_t k = lead_keys[t];
+      int r = 0;
+      for (int j = 0; j < leads; ++j) r += lead_keys[j] > k ? 1 : 0;
+      if (r == a.top - 1 && k) bound = k;
+    }
+    __syncthreads();
+    const uint64_t b = bound;
+    for (int i = t; i < total; i += kThreads) {
+      const uint64_t k = src[i];
+      if (k >= b) keys[atomicAdd(&count, 1)] = k;
+    }
+    __syncthreads();
+    const int n = count;
+    for (int i = t; i < n; i += kThreads) {
+      const uint64_t k = keys[i];
+      int r = 0;
+      for (int j = 0; j < n; ++j) r += keys[j] > k ? 1 : 0;
+      if (r < a.top) best[r] = k;
+    }
+    __syncthreads();
+    store_top(a, row, best, o);
   }
 }
 
@@ -179,12 +520,6 @@ __global__ __launch_bounds__(256) void k_logprob_fwd(LogprobArgs a) {
 struct GradRow {
   float m, nls, k1, k0, add;
   int32_t target;   // column within the tile, out of [0, 128) if elsewhere
-};
-
-// Raw logits of a thread's chunks.
-template <bool F32>
-struct RawChunk {
-  uint4 w[F32 ? 2 : 1];
 };
 
 template <class F, bool F32, bool FULL>
@@ -276,13 +611,33 @@ __global__ __launch_bounds__(kTileThreads) void k_logprob_bwd(LogprobArgs a) {
 
 // ---------------------------------------------------------------- launch
 
-int64_t logprob_work(int64_t, int64_t, int32_t) { return 0; }
+// Few rows are split over the vocabulary so that about 1024 workgroups run
+// (4 per CU), into segments of at least 4096 logits.
+static Split split_rows(int64_t rows, int64_t vocab) {
+  int64_t parts = 1;
+  while (parts < kMaxParts && rows * parts < 1024 && vocab / (2 * parts) >= 4096) parts *= 2;
+  const int64_t seg = ((vocab + parts - 1) / parts + 7) / 8 * 8;
+  return Split{(int32_t)((vocab + seg - 1) / seg), seg};
+}
+
+int64_t logprob_work(int64_t rows, int64_t vocab, int32_t top) {
+  const Split sp = split_rows(rows, vocab);
+  return sp.parts == 1 ? 0 : soft_bytes(rows, sp.parts) + rows * sp.parts * top * (int64_t)sizeof(uint64_t);
+}
+
+template <bool F32, bool TOP>
+static hipError_t launch_fwd(const LogprobArgs& a, hipStream_t s) {
+  const Split sp = split_rows(a.rows, a.vocab);
+  hipLaunchKernelGGL((k_logprob_part<F32, TOP>), dim3((unsigned)(a.rows * sp.parts)), dim3(kThreads), 0, s, a, sp);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || sp.parts == 1) return e;
+  hipLaunchKernelGGL((k_logprob_join<F32, TOP>), dim3((unsigned)a.rows), dim3(kThreads), 0, s, a, sp);
+  return hipGetLastError();
+}
 
 hipError_t launch_logprob_fwd(const LogprobArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.rows);
-  if (a.f32) hipLaunchKernelGGL(k_logprob_fwd<true>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(k_logprob_fwd<false>, grid, dim3(256), 0, s, a);
-  return hipGetLastError();
+  if (a.f32) return a.top ? launch_fwd<true, true>(a, s) : launch_fwd<true, false>(a, s);
+  return a.top ? launch_fwd<false, true>(a, s) : launch_fwd<false, false>(a, s);
 }
 
 hipError_t launch_logprob_bwd(const LogprobArgs& a, hipStream_t s) {
