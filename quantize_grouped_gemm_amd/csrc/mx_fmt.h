@@ -259,6 +259,35 @@ __device__ __forceinline__ void fmt_row(const uint4 (&v)[kTileChunks], uint32_t*
   if ((int)threadIdx.x < kTR) fmt_scales<F>(s_row, threadIdx.x, rows_valid, cols_valid, orow, r0, crow);
 }
 
+// Quantizes one chunk of row `row` at column `col` (a multiple of 8) and
+// stores its codes and its block's or step's scales. All lanes must reach
+// this function; `ok` (uniform over each quad) guards the stores.
+template <class F>
+__device__ __forceinline__ void fmt_chunk(uint4 v, bool ok, const TileOut& o, int64_t row, uint32_t col) {
+  const uint32_t m = quad_max_hi(absmax8_hi(v));
+  uint32_t sb;
+  uint2 codes;
+  if (!__any(m >= kNonFiniteHi)) {
+    sb = scale_byte_hi<F::rceil>(m);
+    codes = chunk_codes<F::rceil>(v, sb);
+  } else {
+    sb = scale_byte(m >> 16, F::rceil);
+    codes = e4m3_chunk(v, sb, !F::rceil);
+  }
+  if constexpr (F::k128) {
+    uint32_t packed = sb << (8 * ((col >> 5) & 3));
+    packed |= dpp<0x124>(packed);
+    packed |= dpp<0x128>(packed);
+    if (ok) {
+      *reinterpret_cast<uint2*>(o.q + row * o.ld + col) = codes;
+      if ((col & 127) == 0) *reinterpret_cast<uint32_t*>(o.s + ((int64_t)(col >> 7) * o.srows + row) * 4) = packed;
+    }
+  } else if (ok) {
+    *reinterpret_cast<uint2*>(o.q + row * o.ld + col) = codes;
+    if ((col & 31) == 0) o.s[row * (o.ld / kBlock) + (col >> 5)] = (uint8_t)sb;
+  }
+}
+
 // Calls f(Fmt<..>{}) for the runtime mode and layout.
 template <class Fn>
 inline void with_fmt(bool rceil, bool k128, Fn f) {

@@ -284,24 +284,48 @@ struct RowOut {
   bool empty;
 };
 
+// Target index (-1: not scored) and its logit; thread 0 only.
+struct TargetLogit {
+  int64_t tg;
+  float x;
+};
+
 template <bool F32>
-__device__ __forceinline__ RowOut store_row(const LogprobArgs& a, int64_t row, Soft v) {
+__device__ __forceinline__ TargetLogit target_logit(const LogprobArgs& a, int64_t row) {
+  TargetLogit r{-1, 0.0f};
+  if (threadIdx.x == 0) {
+    const void* x = logits_row<F32>(a, row);
+    r.tg = row_target(a, row);
+    if (a.dev_err && r.tg < 0 && a.targets[row] != a.ignore_index) atomicOr(a.dev_err, 8);
+    if (r.tg >= 0)
+      r.x = F32 ? static_cast<const float*>(x)[r.tg]
+                : __uint_as_float((uint32_t)static_cast<const uint16_t*>(x)[r.tg] << 16);
+  }
+  return r;
+}
+
+__device__ __forceinline__ RowOut store_row(const LogprobArgs& a, int64_t row, Soft v, TargetLogit tl) {
   const bool empty = v.m == -INFINITY && v.s == 0.0f;
   const float ls = empty ? -INFINITY : logf(v.s);
   if (threadIdx.x == 0) {
-    const void* x = logits_row<F32>(a, row);
-    const int64_t tg = row_target(a, row);
-    if (a.dev_err && tg < 0 && a.targets[row] != a.ignore_index) atomicOr(a.dev_err, 8);
-    float xt = 0.0f;
-    if (tg >= 0)
-      xt = F32 ? static_cast<const float*>(x)[tg]
-               : __uint_as_float((uint32_t)static_cast<const uint16_t*>(x)[tg] << 16);
-    a.logp[row] = tg < 0 ? 0.0f : empty ? -INFINITY : (xt - v.m) * a.scale - ls;
+    a.logp[row] = tl.tg < 0 ? 0.0f : empty ? -INFINITY : (tl.x - v.m) * a.scale - ls;
     a.entropy[row] = empty ? 0.0f : ls - kLn2 * (v.a / v.s);
     a.stats_out[2 * row] = v.m;
     a.stats_out[2 * row + 1] = ls;
   }
   return RowOut{v.m, ls, empty};
+}
+
+// Joins the Softs of a wave's first 32 lanes (every wave does the same work)
+// and stores the row.
+template <bool F32>
+__device__ __forceinline__ RowOut join_row(const LogprobArgs& a, int64_t row, Soft v, float c) {
+  const TargetLogit tl = target_logit<F32>(a, row);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1)
+    v = soft_join(v, Soft{__shfl_xor(v.m, o), __shfl_xor(v.s, o), __shfl_xor(v.a, o)}, c);
+  v = Soft{__shfl(v.m, 0), __shfl(v.s, 0), __shfl(v.a, 0)};
+  return store_row(a, row, v, tl);
 }
 
 __device__ __forceinline__ void store_top(const LogprobArgs& a, int64_t row, const uint64_t* sorted, RowOut o) {
@@ -374,6 +398,8 @@ __global__ __launch_bounds__(kThreads) void k_logprob_part(LogprobArgs a, Split 
     }
   };
   fetch(0, cur);
+  TargetLogit tl{-1, 0.0f};
+  if (sp.parts == 1) tl = target_logit<F32>(a, row);
   int slot = 0, left = per_slot;
   for (int tile = 0; tile < tiles; ++tile) {
     if (tile + 1 < tiles) fetch(tile + 1, nxt);
@@ -445,7 +471,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob_part(LogprobArgs a, Split 
 
   if constexpr (TOP) find_top<F32>(l, x, n, (uint32_t)first, tmax, slot, per_slot, a.top);
   if (sp.parts == 1) {
-    const RowOut o = store_row<F32>(a, row, v);
+    const RowOut o = store_row(a, row, v, tl);
     if constexpr (TOP) store_top(a, row, l.cand, o);
   } else {
     const PartWork w = part_work(a, sp);
@@ -460,53 +486,57 @@ constexpr int kMaxParts = 32;
 
 // One workgroup per row. The alternatives: the top-th largest of the lists'
 // first entries (`lead` of each, at least `top` in all) bounds the result from
-// below; what reaches it, rarely many more than `top`, is ranked.
+// below; what reaches it, rarely many more than `top`, is ranked. All loads of
+// global memory are issued at the start: the kernel is a chain of latencies.
 template <bool F32, bool TOP>
 __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobArgs a, Split sp) {
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, lane = t & 63;
   const int64_t row = blockIdx.x;
   const PartWork w = part_work(a, sp);
   const float c = a.scale * kLog2e;
-  const Soft* parts = w.soft + row * sp.parts;
-  Soft v = parts[0];
-  for (int i = 1; i < sp.parts; ++i) v = soft_join(v, parts[i], c);
-  const RowOut o = store_row<F32>(a, row, v);
+  Soft v{-INFINITY, 0.0f, 0.0f};
+  if (lane < sp.parts) v = w.soft[row * sp.parts + lane];
   if constexpr (TOP) {
-    __shared__ uint64_t keys[kMaxParts * kMaxTop], lead_keys[kThreads], best[kMaxTop];
+    __shared__ uint64_t keys[kMaxParts * kMaxTop], cand[kMaxParts * kMaxTop], best[kMaxTop];
     __shared__ uint64_t bound;
     __shared__ int count;
     const int total = sp.parts * a.top;
     const uint64_t* src = w.keys + row * total;
-    const int lead = min((2 * a.top + sp.parts - 1) / sp.parts, a.top);
-    const int leads = lead * sp.parts;   // at most 2 top + parts
-    if (t < leads) lead_keys[t] = src[(t / lead) * a.top + t % lead];
+    for (int i = t; i < total; i += kThreads) keys[i] = src[i];
     if (t == 0) {
       bound = 1;
       count = 0;
     }
+    const RowOut o = join_row<F32>(a, row, v, c);
+    const int lead = min((2 * a.top + sp.parts - 1) / sp.parts, a.top);
+    const int leads = lead * sp.parts;   // at most 2 top + parts
+    const int at = t < leads ? (t / lead) * a.top + t % lead : 0;
     __syncthreads();
     if (t < leads) {
-      const uint64_t k = lead_keys[t];
+      const uint64_t k = keys[at];
       int r = 0;
-      for (int j = 0; j < leads; ++j) r += lead_keys[j] > k ? 1 : 0;
+      for (int i = 0; i < sp.parts; ++i)
+        for (int j = 0; j < lead; ++j) r += keys[i * a.top + j] > k ? 1 : 0;
       if (r == a.top - 1 && k) bound = k;
     }
     __syncthreads();
     const uint64_t b = bound;
     for (int i = t; i < total; i += kThreads) {
-      const uint64_t k = src[i];
-      if (k >= b) keys[atomicAdd(&count, 1)] = k;
+      const uint64_t k = keys[i];
+      if (k >= b) cand[atomicAdd(&count, 1)] = k;
     }
     __syncthreads();
     const int n = count;
     for (int i = t; i < n; i += kThreads) {
-      const uint64_t k = keys[i];
+      const uint64_t k = cand[i];
       int r = 0;
-      for (int j = 0; j < n; ++j) r += keys[j] > k ? 1 : 0;
+      for (int j = 0; j < n; ++j) r += cand[j] > k ? 1 : 0;
       if (r < a.top) best[r] = k;
     }
     __syncthreads();
     store_top(a, row, best, o);
+  } else {
+    join_row<F32>(a, row, v, c);
   }
 }
 

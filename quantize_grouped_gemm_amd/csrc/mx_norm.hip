@@ -1,13 +1,14 @@
 // Residual addition + RMS norm + MX quantization, and its gradient:
 //   k_norm_row    s = x + r, rstd, row-wise codes of y and of s (checkpoint)
 //   k_norm_bwd    dx, its row-wise codes, partial sums of dw
-//   k_norm_dw     joins the partial sums of dw
-//   k_norm_col    column-wise codes of y (recomputed from s and rstd) or dx
+//   k_norm_tail   column-wise codes of y (recomputed from s and rstd) or of
+//                 dx, and the join of dw's partial sums
 //
 // Row-wise work needs the whole row's statistic before its first output, and
 // column-wise blocks span 32 rows, so the two directions are two launches:
-// the row kernels hold whole rows in registers (mx_row.h), the column kernel
-// reads s or dx back in 128 x 128 tiles (mx_tile.h).
+// the row kernels hold whole rows in registers (mx_row.h), the tail reads s or
+// dx back in 128 x 128 tiles (mx_fmt.h), in reverse order, the rows written
+// last first: they are the ones still in the Infinity Cache.
 
 #include "mx_device.h"
 #include "mx_fmt.h"
@@ -15,26 +16,71 @@
 #include "mx_row.h"
 #include "mx_tile.h"
 
+#include <algorithm>
+
 namespace mxk {
 
-// 256 threads = 4 / WAVES rows per workgroup, NCH chunks per lane.
-template <int WAVES, int NCH>
-__global__ __launch_bounds__(256) void k_norm_row(NormFwdArgs a) {
-  __shared__ float buf[4];
-  const int lane = threadIdx.x & (64 * WAVES - 1);
-  const int64_t row = (int64_t)blockIdx.x * (4 / WAVES) + threadIdx.x / (64 * WAVES);
+// A row belongs to `waves` waves of a workgroup, each thread holding NCH
+// chunks of it; a workgroup has `groups` such rows at a time.
+struct RowShape {
+  int waves, groups, nch;
+};
+
+static RowShape row_shape(int64_t cols) {
+  const int nch = cols <= 8192 ? 1 : 2;   // at most 16 waves a row
+  const int waves = (int)((cols + 512 * nch - 1) / (512 * nch));
+  return RowShape{waves, std::max(1, 4 / waves), nch};
+}
+
+// Where this thread works: its group's index in the grid, its place in the row.
+struct RowPlace {
+  int64_t group;
+  uint32_t lane, threads;   // thread within the group, threads of the group
+  int first_wave;
+};
+
+__device__ __forceinline__ RowPlace row_place(int waves) {
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = w / waves;
+  const int groups = (int)(blockDim.x >> 6) / waves;
+  return RowPlace{(int64_t)blockIdx.x * groups + g, (uint32_t)(threadIdx.x - 64 * g * waves), (uint32_t)(64 * waves),
+                  g * waves};
+}
+
+// Sum over the waves of this thread's group; every thread of the workgroup
+// calls it. `buf`: one value per wave, free again at the next barrier.
+template <class T>
+__device__ __forceinline__ T group_sum(T v, const RowPlace& p, int waves, T* buf) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
+  if (waves > 1) {
+    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = buf[p.first_wave];
+    for (int i = 1; i < waves; ++i) v += buf[p.first_wave + i];
+  }
+  return v;
+}
+
+template <class F, int NCH>
+__global__ __launch_bounds__(1024) void k_norm_row(NormFwdArgs a, int waves) {
+  __shared__ double buf[16];
+  const RowPlace p = row_place(waves);
+  const int64_t row = p.group;
   const bool live = row < a.rows;
   uint4 v[NCH];
+  float w[NCH][8];
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int col = 8 * (lane + 64 * WAVES * i);
+    const uint32_t col = 8 * (p.lane + p.threads * i);
     const bool ok = live && col < a.cols;
     v[i] = ok ? load_stream16(a.x + row * a.ld_x + col) : make_uint4(0, 0, 0, 0);
+    const uint4 u = ok && a.r ? load_stream16(a.r + row * a.ld_r + col) : make_uint4(0, 0, 0, 0);
+    if (ok) load8f(a.w + col, w[i]);
     float f[8];
     unpack8(v[i], f);
     if (a.r) {
-      const uint4 u = ok ? load_stream16(a.r + row * a.ld_r + col) : make_uint4(0, 0, 0, 0);
       float g[8];
       unpack8(u, g);
 #pragma unroll
@@ -46,125 +92,152 @@ __global__ __launch_bounds__(256) void k_norm_row(NormFwdArgs a) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) ss = fmaf(f[k], f[k], ss);
   }
-  ss = group_sum<WAVES>(ss, buf);
-  const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
-  if (live && lane == 0) a.rstd[row] = rstd;
-  const TileOut orow{a.q_row, a.s_row, a.cols, a.rows, a.k128};
-  const TileOut ock{a.q_ck, a.s_ck, a.cols, a.rows, a.k128};
+  // Each thread's sum of at most 16 squares in float32, their join and the
+  // root in float64: rstd is then the correctly rounded value but for rare
+  // ties. Float32 throughout leaves it an ulp off, which every value of the
+  // row shares.
+  const double ms = group_sum<double>((double)ss, p, waves, buf) / (double)a.cols + (double)a.eps;
+  double rs = (double)(1.0f / sqrtf((float)ms));
+  if (rs > 0.0 && ms > 0.0 && rs < INFINITY) rs = fma(0.5 * rs, fma(-ms * rs, rs, 1.0), rs);   // Newton
+  const float rstd = (float)rs;
+  if (live && p.lane == 0) a.rstd[row] = rstd;
+  const TileOut orow{a.q_row, a.s_row, a.cols, a.rows, F::k128};
+  const TileOut ock{a.q_ck, a.s_ck, a.cols, a.rows, F::k128};
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int col = 8 * (lane + 64 * WAVES * i);
+    const uint32_t col = 8 * (p.lane + p.threads * i);
     const bool ok = live && col < a.cols;
-    if (a.q_ck) chunk_rowq(v[i], ok, a.rceil, ock, row, col);
-    float w[8] = {};
-    if (ok) load8f(a.w + col, w);
-    chunk_rowq(norm_chunk(v[i], rstd, w), ok, a.rceil, orow, row, col);
+    if (a.q_ck) fmt_chunk<F>(v[i], ok, ock, row, col);
+    fmt_chunk<F>(ok ? norm_chunk(v[i], rstd, w[i]) : make_uint4(0, 0, 0, 0), ok, orow, row, col);
   }
 }
 
-// Rows per partial sum of dw.
-constexpr int64_t kDwRows = 16;
+// Rows per partial sum of dw: one partial sum a group, 16 rows at most, fewer
+// where that would leave less than 4096 waves (16 a CU) to hide the latency of
+// memory; each partial sum costs a row of float32 written and read.
+static int64_t part_rows(int64_t rows, int64_t cols) {
+  const int64_t r = (rows * row_shape(cols).waves + 4095) / 4096;
+  return std::min<int64_t>(std::max<int64_t>(r, 1), 16);
+}
 
-static int64_t dw_parts(int64_t rows) { return (rows + kDwRows - 1) / kDwRows; }
+static int64_t dw_parts(int64_t rows, int64_t cols) {
+  const int64_t r = part_rows(rows, cols);
+  return (rows + r - 1) / r;
+}
 
-template <int WAVES, int NCH, bool CK>
-__global__ __launch_bounds__(256) void k_norm_bwd(NormBwdArgs a) {
-  __shared__ float buf[2][4];
-  const int lane = threadIdx.x & (64 * WAVES - 1);
-  const int64_t part = (int64_t)blockIdx.x * (4 / WAVES) + threadIdx.x / (64 * WAVES);
-  float dw[NCH][8] = {};
+// What a thread reads of a row.
+template <int NCH, bool CK>
+struct BwdRow {
+  uint4 dy[NCH], ds[NCH], x[CK ? 1 : NCH];
+  uint2 q[CK ? NCH : 1];
+  uint32_t sb[CK ? NCH : 1];
+  float rstd;
+};
+
+template <class F, int NCH, bool CK>
+__device__ __forceinline__ void bwd_load(BwdRow<NCH, CK>& b, const NormBwdArgs& a, const RowPlace& p, int64_t row) {
+  const bool live = row < a.rows;
+  b.rstd = live ? a.rstd[row] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const uint32_t col = 8 * (p.lane + p.threads * i);
+    const bool ok = live && col < a.cols;
+    b.dy[i] = ok ? load_stream16(a.dy + row * a.ld_dy + col) : make_uint4(0, 0, 0, 0);
+    b.ds[i] = ok && a.dsum ? load_stream16(a.dsum + row * a.ld_dsum + col) : make_uint4(0, 0, 0, 0);
+    if constexpr (CK) {
+      b.q[i] = make_uint2(0, 0);
+      b.sb[i] = 0;
+      if (ok) {
+        b.q[i] = *reinterpret_cast<const uint2*>(a.q_ck + row * a.cols + col);
+        b.sb[i] = F::k128 ? a.s_ck[((int64_t)(col >> 7) * a.rows + row) * 4 + ((col >> 5) & 3)]
+                          : a.s_ck[row * (a.cols / kBlock) + (col >> 5)];
+      }
+    } else {
+      b.x[i] = ok ? load_stream16(a.x + row * a.ld_x + col) : make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+// A group takes `rows` consecutive rows, the next one's loads in flight while
+// it works on one (with one chunk a thread; two would spill); dw's sums over
+// them stay in registers.
+template <class F, int NCH, bool CK>
+__global__ __launch_bounds__(1024) void k_norm_bwd(NormBwdArgs a, int waves, int rows) {
+  __shared__ float buf[2][16];
+  const RowPlace p = row_place(waves);
+  const int64_t row0 = p.group * rows;
+  float dw[NCH][8] = {}, w[NCH][8] = {};
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const uint32_t col = 8 * (p.lane + p.threads * i);
+    if (col < a.cols) load8f(a.w + col, w[i]);
+  }
   const float inv_n = 1.0f / (float)a.cols;
-  const TileOut orow{a.q_row, a.s_row, a.cols, a.rows, a.k128};
-  for (int rr = 0; rr < kDwRows; ++rr) {
-    const int64_t row = part * kDwRows + rr;
+  const TileOut orow{a.q_row, a.s_row, a.cols, a.rows, F::k128};
+  BwdRow<NCH, CK> cur, nxt;
+  bwd_load<F>(cur, a, p, row0);
+  for (int rr = 0; rr < rows; ++rr) {
+    const int64_t row = row0 + rr;
     const bool live = row < a.rows;
-    const float rstd = live ? a.rstd[row] : 0.0f;
-    uint4 dy[NCH];
-    float xh[NCH][8];
+    if (NCH == 1 && rr + 1 < rows) bwd_load<F>(nxt, a, p, row + 1);
+    float xh[NCH][8], g[NCH][8];
     float c = 0.0f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int col = 8 * (lane + 64 * WAVES * i);
-      const bool ok = live && col < a.cols;
-      dy[i] = ok ? load_stream16(a.dy + row * a.ld_dy + col) : make_uint4(0, 0, 0, 0);
-      if constexpr (CK) {
-        uint2 q = make_uint2(0, 0);
-        uint32_t sb = 0;
-        if (ok) {
-          q = *reinterpret_cast<const uint2*>(a.q_ck + row * a.cols + col);
-          sb = a.k128 ? a.s_ck[((int64_t)(col >> 7) * a.rows + row) * 4 + ((col >> 5) & 3)]
-                      : a.s_ck[row * (a.cols / kBlock) + (col >> 5)];
-        }
-        e4m3_chunk_values(q, sb, xh[i]);
-      } else {
-        unpack8(ok ? load_stream16(a.x + row * a.ld_x + col) : make_uint4(0, 0, 0, 0), xh[i]);
-      }
-      float w[8] = {}, d[8];
-      if (ok) load8f(a.w + col, w);
-      unpack8(dy[i], d);
+      float d[8];
+      if constexpr (CK) e4m3_chunk_values(cur.q[i], cur.sb[i], xh[i]);
+      else unpack8(cur.x[i], xh[i]);
+      unpack8(cur.dy[i], d);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        xh[i][k] *= rstd;
-        c = fmaf(d[k] * w[k], xh[i][k], c);
+        xh[i][k] *= cur.rstd;
+        g[i][k] = d[k] * w[i][k];
+        c = fmaf(g[i][k], xh[i][k], c);
         dw[i][k] = fmaf(d[k], xh[i][k], dw[i][k]);
       }
     }
-    c = group_sum<WAVES>(c, buf[rr & 1]) * inv_n;
+    c = group_sum<float>(c, p, waves, buf[rr & 1]) * inv_n;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int col = 8 * (lane + 64 * WAVES * i);
+      const uint32_t col = 8 * (p.lane + p.threads * i);
       const bool ok = live && col < a.cols;
-      float w[8] = {}, d[8], e[8] = {};
-      if (ok) load8f(a.w + col, w);
-      unpack8(dy[i], d);
-      if (a.dsum && ok) unpack8(load_stream16(a.dsum + row * a.ld_dsum + col), e);
+      float e[8];
+      unpack8(cur.ds[i], e);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) e[k] = fmaf(fmaf(-xh[i][k], c, d[k] * w[k]), rstd, e[k]);
+      for (int k = 0; k < 8; ++k) e[k] = fmaf(fmaf(-xh[i][k], c, g[i][k]), cur.rstd, e[k]);
       const uint4 v = pack8(e);
       if (ok) *reinterpret_cast<uint4*>(a.dx + row * a.cols + col) = v;
-      if (a.q_row) chunk_rowq(v, ok, a.rceil, orow, row, col);
+      if (a.q_row) fmt_chunk<F>(v, ok, orow, row, col);
     }
+    if (NCH == 1) cur = nxt;
+    else if (rr + 1 < rows) bwd_load<F>(cur, a, p, row + 1);
   }
-  if (part * kDwRows < a.rows) {
+  if (row0 < a.rows) {
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int col = 8 * (lane + 64 * WAVES * i);
+      const uint32_t col = 8 * (p.lane + p.threads * i);
       if (col < a.cols) {
-        float4* p = reinterpret_cast<float4*>(a.work + part * a.cols + col);
-        p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-        p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+        float4* out = reinterpret_cast<float4*>(a.work + p.group * a.cols + col);
+        out[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+        out[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
       }
     }
   }
 }
 
-// dw[c] = sum over the parts of work[part, c]: 32 columns per workgroup, 32
-// threads down each, joined in LDS in a fixed order.
-__global__ __launch_bounds__(1024) void k_norm_dw(const float* work, int64_t parts, int64_t cols, float* dw) {
-  __shared__ float acc[32][33];
-  const int c = threadIdx.x & 31, p0 = threadIdx.x >> 5;
-  const int64_t col = (int64_t)blockIdx.x * 32 + c;
-  float s = 0.0f;
-  for (int64_t p = p0; p < parts; p += 32) s += work[p * cols + col];
-  acc[p0][c] = s;
-  __syncthreads();
-  if (p0 == 0) {
-    float t = 0.0f;
-    for (int i = 0; i < 32; ++i) t += acc[i][c];
-    dw[col] = t;
-  }
-}
-
-struct NormColArgs {
-  const uint16_t* x;
+struct NormTailArgs {
+  const uint16_t* x;         // s or dx
   int64_t ld, rows, rows_pad, cols;
-  const float *rstd, *w;     // NULL: quantize x itself
-  bool rceil, k128;
-  uint8_t *q, *s;
+  const float *rstd, *w;     // forward
+  uint8_t *q, *s;            // NULL: no column-wise codes
+  int32_t dw_blocks;         // workgroups that join dw, ahead of the tiles
+  const float* work;
+  int64_t parts;
+  float* dw;
 };
 
 template <class F, bool NORM, bool FULL>
-__device__ __forceinline__ void norm_col_tile(const NormColArgs& a, TileLds& l, int64_t r0, int64_t c0, int rows_valid,
+__device__ __forceinline__ void norm_col_tile(const NormTailArgs& a, TileLds& l, int64_t r0, int64_t c0, int rows_valid,
                                               int rows_pad, int cols_valid) {
   uint4 v[kTileChunks];
   fmt_load<FULL>(v, a.x + r0 * a.ld + c0, a.ld, rows_valid, cols_valid);
@@ -187,11 +260,42 @@ __device__ __forceinline__ void norm_col_tile(const NormColArgs& a, TileLds& l, 
   if (t < kTC) fmt_scales<F>(l.s_col, t, cols_valid, rows_pad, o, c0, r0);
 }
 
+// dw[c] = sum over the parts of work[part, c]: 32 columns per workgroup, 32
+// threads down each group of 4, joined in LDS in a fixed order.
+__device__ __forceinline__ void join_dw(const NormTailArgs& a, float4* acc) {
+  const int c = threadIdx.x & 7, p0 = threadIdx.x >> 3;
+  const float4* src = reinterpret_cast<const float4*>(a.work + (int64_t)blockIdx.x * 32) + c;
+  const int64_t ld = a.cols / 4;
+  auto add = [](float4 u, float4 v) { return make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w); };
+  float4 s0 = make_float4(0, 0, 0, 0), s1 = s0, s2 = s0, s3 = s0;
+  int64_t p = p0;
+  for (; p + 96 < a.parts; p += 128) {
+    s0 = add(s0, src[p * ld]);
+    s1 = add(s1, src[(p + 32) * ld]);
+    s2 = add(s2, src[(p + 64) * ld]);
+    s3 = add(s3, src[(p + 96) * ld]);
+  }
+  for (; p < a.parts; p += 32) s0 = add(s0, src[p * ld]);
+  acc[threadIdx.x] = add(add(s0, s1), add(s2, s3));
+  __syncthreads();
+  if (p0 == 0) {
+    float4 t = make_float4(0, 0, 0, 0);
+    for (int i = 0; i < 32; ++i) t = add(t, acc[8 * i + c]);
+    reinterpret_cast<float4*>(a.dw + (int64_t)blockIdx.x * 32)[c] = t;
+  }
+}
+
 template <class F, bool NORM>
-__global__ __launch_bounds__(kTileThreads) void k_norm_col(NormColArgs a) {
+__global__ __launch_bounds__(kTileThreads) void k_norm_tail(NormTailArgs a) {
   __shared__ TileLds l;
-  const int64_t r0 = (int64_t)blockIdx.y * kTR;
-  const int64_t c0 = (int64_t)blockIdx.x * kTC;
+  if ((int)blockIdx.x < a.dw_blocks) {
+    join_dw(a, reinterpret_cast<float4*>(l.v));
+    return;
+  }
+  const uint32_t b = gridDim.x - 1 - blockIdx.x;   // the last tile first
+  const uint32_t per_row = (uint32_t)((a.cols + kTC - 1) / kTC);
+  const int64_t r0 = (int64_t)(b / per_row) * kTR;
+  const int64_t c0 = (int64_t)(b % per_row) * kTC;
   const int rows_valid = (int)min<int64_t>(kTR, a.rows - r0);
   const int rows_pad = (int)min<int64_t>(kTR, a.rows_pad - r0);
   const int cols_valid = (int)min<int64_t>(kTC, a.cols - c0);
@@ -203,65 +307,63 @@ __global__ __launch_bounds__(kTileThreads) void k_norm_col(NormColArgs a) {
 
 // ---------------------------------------------------------------- launch
 
-// Calls f with std::integral_constant-like tags: the waves of a row and the
-// chunks of a lane. Rows of up to 512 values fit one wave; longer ones are
-// spread over 4 waves.
-template <int W, int N>
-struct RowShape {
-  static constexpr int waves = W, chunks = N;
-};
-
-template <class F>
-static void with_row_shape(int64_t cols, F f) {
-  if (cols <= 512) f(RowShape<1, 1>{});
-  else if (cols <= 2048) f(RowShape<4, 1>{});
-  else if (cols <= 4096) f(RowShape<4, 2>{});
-  else if (cols <= 6144) f(RowShape<4, 3>{});
-  else if (cols <= 8192) f(RowShape<4, 4>{});
-  else f(RowShape<4, 8>{});
-}
-
 template <bool NORM>
-static void launch_col(const NormColArgs& c, hipStream_t s) {
-  const dim3 grid((unsigned)((c.cols + kTC - 1) / kTC), (unsigned)((c.rows_pad + kTR - 1) / kTR));
-  with_fmt(c.rceil, c.k128, [&](auto f) {
-    hipLaunchKernelGGL((k_norm_col<decltype(f), NORM>), grid, dim3(kTileThreads), 0, s, c);
+static hipError_t launch_tail(const NormTailArgs& c, bool rceil, bool k128, hipStream_t s) {
+  const int64_t tiles = c.q ? (c.cols + kTC - 1) / kTC * ((c.rows_pad + kTR - 1) / kTR) : 0;
+  const dim3 grid((unsigned)(c.dw_blocks + tiles));
+  with_fmt(rceil, k128, [&](auto f) {
+    hipLaunchKernelGGL((k_norm_tail<decltype(f), NORM>), grid, dim3(kTileThreads), 0, s, c);
   });
-}
-
-hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t s) {
-  with_row_shape(a.cols, [&](auto sh) {
-    constexpr int kRows = 4 / decltype(sh)::waves;
-    hipLaunchKernelGGL((k_norm_row<decltype(sh)::waves, decltype(sh)::chunks>),
-                       dim3((unsigned)((a.rows + kRows - 1) / kRows)), dim3(256), 0, s, a);
-  });
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.q_col) return e;
-  launch_col<true>(NormColArgs{a.r ? a.sum : a.x, a.r ? a.cols : a.ld_x, a.rows, a.rows_pad, a.cols, a.rstd, a.w,
-                               a.rceil, a.k128, a.q_col, a.s_col}, s);
   return hipGetLastError();
 }
 
-int64_t norm_bwd_work(int64_t rows, int64_t cols) { return dw_parts(rows) * cols; }
+hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t s) {
+  const RowShape sh = row_shape(a.cols);
+  const dim3 grid((unsigned)((a.rows + sh.groups - 1) / sh.groups)), block(64 * sh.waves * sh.groups);
+  with_fmt(a.rceil, a.k128, [&](auto f) {
+    using F = decltype(f);
+    if (sh.nch == 1) hipLaunchKernelGGL((k_norm_row<F, 1>), grid, block, 0, s, a, sh.waves);
+    else hipLaunchKernelGGL((k_norm_row<F, 2>), grid, block, 0, s, a, sh.waves);
+  });
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.q_col) return e;
+  NormTailArgs c{};
+  c.x = a.r ? a.sum : a.x;
+  c.ld = a.r ? a.cols : a.ld_x;
+  c.rows = a.rows; c.rows_pad = a.rows_pad; c.cols = a.cols;
+  c.rstd = a.rstd; c.w = a.w; c.q = a.q_col; c.s = a.s_col;
+  return launch_tail<true>(c, a.rceil, a.k128, s);
+}
+
+int64_t norm_bwd_work(int64_t rows, int64_t cols) { return dw_parts(rows, cols) * cols; }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t s) {
-  const int64_t parts = dw_parts(a.rows);
+  const RowShape sh = row_shape(a.cols);
+  const int64_t parts = a.rows ? dw_parts(a.rows, a.cols) : 0;
   if (parts > 0) {
-    with_row_shape(a.cols, [&](auto sh) {
-      constexpr int W = decltype(sh)::waves, N = decltype(sh)::chunks, kParts = 4 / W;
-      const dim3 grid((unsigned)((parts + kParts - 1) / kParts));
-      if (a.q_ck) hipLaunchKernelGGL((k_norm_bwd<W, N, true>), grid, dim3(256), 0, s, a);
-      else hipLaunchKernelGGL((k_norm_bwd<W, N, false>), grid, dim3(256), 0, s, a);
+    const int per = (int)part_rows(a.rows, a.cols);
+    const dim3 grid((unsigned)((parts + sh.groups - 1) / sh.groups)), block(64 * sh.waves * sh.groups);
+    with_fmt(a.rceil, a.k128, [&](auto f) {
+      using F = decltype(f);
+      if (sh.nch == 1) {
+        if (a.q_ck) hipLaunchKernelGGL((k_norm_bwd<F, 1, true>), grid, block, 0, s, a, sh.waves, per);
+        else hipLaunchKernelGGL((k_norm_bwd<F, 1, false>), grid, block, 0, s, a, sh.waves, per);
+      } else {
+        if (a.q_ck) hipLaunchKernelGGL((k_norm_bwd<F, 2, true>), grid, block, 0, s, a, sh.waves, per);
+        else hipLaunchKernelGGL((k_norm_bwd<F, 2, false>), grid, block, 0, s, a, sh.waves, per);
+      }
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)(a.cols / 32)), dim3(1024), 0, s, a.work, parts, a.cols, a.dw);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.q_col || parts == 0) return e;
-  launch_col<false>(NormColArgs{a.dx, a.cols, a.rows, a.rows_pad, a.cols, nullptr, nullptr, a.rceil, a.k128, a.q_col,
-                                a.s_col}, s);
-  return hipGetLastError();
+  NormTailArgs c{};
+  c.x = a.dx;
+  c.ld = a.cols;
+  c.rows = a.rows; c.rows_pad = a.rows_pad; c.cols = a.cols;
+  c.q = parts ? a.q_col : nullptr; c.s = a.s_col;
+  c.dw_blocks = (int32_t)(a.cols / 32);
+  c.work = a.work; c.parts = parts; c.dw = a.dw;
+  return launch_tail<false>(c, a.rceil, a.k128, s);
 }
 
 }  // namespace mxk
