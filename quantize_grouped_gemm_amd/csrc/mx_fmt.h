@@ -1,8 +1,11 @@
-// MX quantization of a 128 x 128 bf16 tile, specialised on the format (scale
-// rounding, scale layout) and on whether the tile is whole. Same tile scheme,
-// LDS swizzle and results as mx_tile.h; the kernels that use it are bound by
-// their VALU issue rate, and here a dual quantization takes about half the
-// instructions:
+// MX quantization of a 128 x 128 bf16 tile by 512 threads, specialised on the
+// format (scale rounding, scale layout) and on whether the tile is whole. Same
+// LDS swizzle and results as mx_tile.h; thread t holds 4 chunks of 8 values,
+// chunk j at tile row (t >> 4) + 32 j, columns 8 (t & 15) .. + 7. LDS holds
+// four tiles a CU, and with 8 waves a tile (64 VGPRs) every SIMD has 8 waves
+// to issue from where 4-wave tiles leave it 4. The kernels that use it are
+// close to their VALU issue rate, and here a dual quantization takes about
+// half the instructions of mx_tile.h:
 //   * mode and layout are template arguments, and a whole tile's loads and
 //     stores carry no per-chunk bounds;
 //   * addresses are a uniform 64-bit base plus a 32-bit lane offset;
@@ -24,6 +27,10 @@ template <bool RCEIL, bool K128>
 struct Fmt {
   static constexpr bool rceil = RCEIL, k128 = K128;
 };
+
+constexpr int kFmtThreads = 512;
+constexpr int kChunks = kTR * kTC / 8 / kFmtThreads;   // 4 per thread
+constexpr int kRowStep = kFmtThreads / 16;              // rows between a thread's chunks
 
 // LDS of one tile: the bf16 values and the scale bytes of both directions
 // (one dword = four blocks per row or column).
@@ -96,36 +103,42 @@ __device__ __forceinline__ uint2 chunk_codes(uint4 v, uint32_t sb) {
 // The thread's chunks of the bf16 tile whose (0,0) is `base` (uniform), row
 // stride ld < 2^27; zeros outside the valid region.
 template <bool FULL>
-__device__ __forceinline__ void fmt_load(uint4 (&v)[kTileChunks], const uint16_t* base, int64_t ld, int rows_valid,
+__device__ __forceinline__ void fmt_load(uint4 (&v)[kChunks], const uint16_t* base, int64_t ld, int rows_valid,
                                          int cols_valid) {
   if constexpr (FULL) {
     const uint32_t t = threadIdx.x;
     const uint32_t off = ((t >> 4) * (uint32_t)ld + (t & 15) * 8) * 2;
 #pragma unroll
-    for (int j = 0; j < kTileChunks; ++j)
-      v[j] = load_stream16(reinterpret_cast<const char*>(base + (int64_t)(16 * j) * ld) + off);
+    for (int j = 0; j < kChunks; ++j)
+      v[j] = load_stream16(reinterpret_cast<const char*>(base + (int64_t)(kRowStep * j) * ld) + off);
   } else {
-    tile_load<true>(v, base, ld, rows_valid, cols_valid);
+    const int t = threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+      const int row = (t >> 4) + kRowStep * j;
+      v[j] = row < rows_valid && (t & 15) * 8 < cols_valid ? load_stream16(base + row * ld + (t & 15) * 8)
+                                                           : make_uint4(0, 0, 0, 0);
+    }
   }
 }
 
 // Row-wise codes of the tile from the threads' chunks; scale bytes to s_row.
 // All threads must reach this function.
 template <class F, bool FULL>
-__device__ __forceinline__ void fmt_rowq(const uint4 (&v)[kTileChunks], int rows_valid, int cols_valid,
+__device__ __forceinline__ void fmt_rowq(const uint4 (&v)[kChunks], int rows_valid, int cols_valid,
                                          const TileOut& o, int64_t r0, int64_t c0, uint32_t* s_row) {
   const uint32_t t = threadIdx.x, cc = t & 15, tr = t >> 4;
   uint8_t* base = o.q + r0 * o.ld + c0;
   const uint32_t off = tr * (uint32_t)o.ld + cc * 8;
-  uint32_t sb[kTileChunks], all = 0;
+  uint32_t sb[kChunks], all = 0;
 #pragma unroll
-  for (int j = 0; j < kTileChunks; ++j) {
+  for (int j = 0; j < kChunks; ++j) {
     sb[j] = quad_max_hi(absmax8_hi(v[j]));
     all = max(all, sb[j]);
   }
   const bool special = __any(all >= kNonFiniteHi);
 #pragma unroll
-  for (int j = 0; j < kTileChunks; ++j) {
+  for (int j = 0; j < kChunks; ++j) {
     uint2 codes;
     if (!special) {
       sb[j] = scale_byte_hi<F::rceil>(sb[j]);
@@ -134,20 +147,26 @@ __device__ __forceinline__ void fmt_rowq(const uint4 (&v)[kTileChunks], int rows
       sb[j] = scale_byte(sb[j] >> 16, F::rceil);
       codes = e4m3_chunk(v[j], sb[j], !F::rceil);
     }
-    if (FULL || ((int)tr + 16 * j < rows_valid && (int)cc * 8 < cols_valid))
-      *reinterpret_cast<uint2*>(base + (int64_t)(16 * j) * o.ld + off) = codes;
+    if (FULL || ((int)tr + kRowStep * j < rows_valid && (int)cc * 8 < cols_valid))
+      *reinterpret_cast<uint2*>(base + (int64_t)(kRowStep * j) * o.ld + off) = codes;
   }
   if ((t & 3) == 0) {
     uint8_t* s = reinterpret_cast<uint8_t*>(s_row) + tr * 4 + (cc >> 2);
 #pragma unroll
-    for (int j = 0; j < kTileChunks; ++j) s[64 * j] = (uint8_t)sb[j];
+    for (int j = 0; j < kChunks; ++j) s[4 * kRowStep * j] = (uint8_t)sb[j];
   }
 }
 
-__device__ __forceinline__ void fmt_to_lds(const uint4 (&v)[kTileChunks], TileLds& l) { tile_to_lds(v, l.v); }
+__device__ __forceinline__ void fmt_to_lds(const uint4 (&v)[kChunks], TileLds& l) {
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < kChunks; ++j) l.v[lds_unit((t >> 4) + kRowStep * j, t & 15)] = v[j];
+}
 
-// Column-wise codes from the LDS copy (work split as in tile_colq); scale
-// bytes to s_col. rows_valid counts the rows that are written, zero rows
+// Column-wise codes from the LDS copy: lane l of wave w takes rows 16 q .. 16 q
+// + 15, q = l & 7, of the columns 2 cp and 2 cp + 1, cp = 8 w + (l >> 3), so the
+// 8 lanes of a column pair cover 128 codes of two output rows; scale bytes to
+// s_col. rows_valid counts the rows that are written, zero rows
 // included.
 template <class F, bool FULL>
 __device__ __forceinline__ void fmt_colq(TileLds& l, int rows_valid, int cols_valid, const TileOut& o, int64_t r0,
@@ -155,62 +174,59 @@ __device__ __forceinline__ void fmt_colq(TileLds& l, int rows_valid, int cols_va
   const uint32_t* lds = reinterpret_cast<const uint32_t*>(l.v);
   const uint32_t lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane & 7;
   uint8_t* base = o.q + c0 * o.ld + r0;
+  const uint32_t cp = 8 * w + (lane >> 3);
+  uint32_t v[16];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const uint32_t cp = 8 * w + (lane >> 3) + 32 * s;
-    uint32_t v[16];
+  for (int r = 0; r < 16; ++r) v[r] = lds[lds_unit(16 * q + r, cp >> 2) * 4 + (cp & 3)];
+  mx_us2 m = __builtin_bit_cast(mx_us2, v[0] & 0x7FFF7FFFu);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) v[r] = lds[lds_unit(16 * q + r, cp >> 2) * 4 + (cp & 3)];
-    mx_us2 m = __builtin_bit_cast(mx_us2, v[0] & 0x7FFF7FFFu);
+  for (int r = 1; r < 16; ++r) m = __builtin_elementwise_max(m, __builtin_bit_cast(mx_us2, v[r] & 0x7FFF7FFFu));
+  m = __builtin_elementwise_max(m, __builtin_bit_cast(mx_us2, dpp<0xB1>(__builtin_bit_cast(uint32_t, m))));
+  const uint32_t m1 = __builtin_bit_cast(uint32_t, m), m0 = m1 << 16;
+  uint32_t sb0, sb1, c0w[4], c1w[4];
+  const bool special = __any(max(m0, m1) >= kNonFiniteHi);
+  if (!special) {
+    sb0 = scale_byte_hi<F::rceil>(m0);
+    sb1 = scale_byte_hi<F::rceil>(m1);
+  } else {
+    sb0 = scale_byte(m0 >> 16, F::rceil);
+    sb1 = scale_byte(m1 >> 16, F::rceil);
+  }
+  if constexpr (!F::rceil) {
+    const uint32_t lim2 = special ? sat_bits(sb0) | (sat_bits(sb1) << 16)
+                                  : __builtin_amdgcn_perm(floor_limit2(sb1), floor_limit2(sb0), 0x07060100u);
 #pragma unroll
-    for (int r = 1; r < 16; ++r) m = __builtin_elementwise_max(m, __builtin_bit_cast(mx_us2, v[r] & 0x7FFF7FFFu));
-    m = __builtin_elementwise_max(m, __builtin_bit_cast(mx_us2, dpp<0xB1>(__builtin_bit_cast(uint32_t, m))));
-    const uint32_t m1 = __builtin_bit_cast(uint32_t, m), m0 = m1 << 16;
-    uint32_t sb0, sb1, c0w[4], c1w[4];
-    const bool special = __any(max(m0, m1) >= kNonFiniteHi);
-    if (!special) {
-      sb0 = scale_byte_hi<F::rceil>(m0);
-      sb1 = scale_byte_hi<F::rceil>(m1);
-    } else {
-      sb0 = scale_byte(m0 >> 16, F::rceil);
-      sb1 = scale_byte(m1 >> 16, F::rceil);
-    }
-    if constexpr (!F::rceil) {
-      const uint32_t lim2 = special ? sat_bits(sb0) | (sat_bits(sb1) << 16)
-                                    : __builtin_amdgcn_perm(floor_limit2(sb1), floor_limit2(sb0), 0x07060100u);
+    for (int r = 0; r < 16; ++r) v[r] = clamp_pair(v[r], lim2);
+  }
+  const float sc0 = scale_of(sb0), sc1 = scale_of(sb1);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) v[r] = clamp_pair(v[r], lim2);
-    }
-    const float sc0 = scale_of(sb0), sc1 = scale_of(sb1);
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t* x = &v[4 * k];
+    c0w[k] = cvt4u(__builtin_amdgcn_perm(x[1], x[0], 0x05040100u), __builtin_amdgcn_perm(x[3], x[2], 0x05040100u), sc0);
+    c1w[k] = cvt4u(__builtin_amdgcn_perm(x[1], x[0], 0x07060302u), __builtin_amdgcn_perm(x[3], x[2], 0x07060302u), sc1);
+  }
+  if (special) {   // blocks with scale 0xFF: 0x7F with each element's sign
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t* x = &v[4 * k];
-      c0w[k] = cvt4u(__builtin_amdgcn_perm(x[1], x[0], 0x05040100u), __builtin_amdgcn_perm(x[3], x[2], 0x05040100u), sc0);
-      c1w[k] = cvt4u(__builtin_amdgcn_perm(x[1], x[0], 0x07060302u), __builtin_amdgcn_perm(x[3], x[2], 0x07060302u), sc1);
-    }
-    if (special) {   // blocks with scale 0xFF: 0x7F with each element's sign
+      uint32_t a = 0x7F7F7F7Fu, b = 0x7F7F7F7Fu;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t a = 0x7F7F7F7Fu, b = 0x7F7F7F7Fu;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a |= ((v[4 * k + i] >> 15) & 1u) << (8 * i + 7);
-          b |= ((v[4 * k + i] >> 31) & 1u) << (8 * i + 7);
-        }
-        if (sb0 == 0xFFu) c0w[k] = a;
-        if (sb1 == 0xFFu) c1w[k] = b;
+      for (int i = 0; i < 4; ++i) {
+        a |= ((v[4 * k + i] >> 15) & 1u) << (8 * i + 7);
+        b |= ((v[4 * k + i] >> 31) & 1u) << (8 * i + 7);
       }
+      if (sb0 == 0xFFu) c0w[k] = a;
+      if (sb1 == 0xFFu) c1w[k] = b;
     }
-    if (FULL || ((int)(2 * cp) < cols_valid && (int)(16 * q) < rows_valid)) {
-      const uint32_t off = 2 * cp * (uint32_t)o.ld + 16 * q;
-      *reinterpret_cast<uint4*>(base + off) = make_uint4(c0w[0], c0w[1], c0w[2], c0w[3]);
-      *reinterpret_cast<uint4*>(base + o.ld + off) = make_uint4(c1w[0], c1w[1], c1w[2], c1w[3]);
-    }
-    if ((lane & 1) == 0) {
-      uint8_t* sp = reinterpret_cast<uint8_t*>(l.s_col) + 8 * cp + (q >> 1);
-      sp[0] = (uint8_t)sb0;
-      sp[4] = (uint8_t)sb1;
-    }
+  }
+  if (FULL || ((int)(2 * cp) < cols_valid && (int)(16 * q) < rows_valid)) {
+    const uint32_t off = 2 * cp * (uint32_t)o.ld + 16 * q;
+    *reinterpret_cast<uint4*>(base + off) = make_uint4(c0w[0], c0w[1], c0w[2], c0w[3]);
+    *reinterpret_cast<uint4*>(base + o.ld + off) = make_uint4(c1w[0], c1w[1], c1w[2], c1w[3]);
+  }
+  if ((lane & 1) == 0) {
+    uint8_t* sp = reinterpret_cast<uint8_t*>(l.s_col) + 8 * cp + (q >> 1);
+    sp[0] = (uint8_t)sb0;
+    sp[4] = (uint8_t)sb1;
   }
 }
 
@@ -236,7 +252,7 @@ __device__ __forceinline__ void fmt_scales(const uint32_t* s, int i, int lines, 
 // rows, the extra ones zeros). Holds barriers; ends with one if `more` work
 // on the same LDS follows.
 template <class F, bool FULL>
-__device__ __forceinline__ void fmt_dual(const uint4 (&v)[kTileChunks], TileLds& l, int rows_valid, int rows_pad,
+__device__ __forceinline__ void fmt_dual(const uint4 (&v)[kChunks], TileLds& l, int rows_valid, int rows_pad,
                                          int cols_valid, const TileOut& orow, const TileOut& ocol, int64_t r0,
                                          int64_t crow, bool more) {
   fmt_rowq<F, FULL>(v, rows_valid, cols_valid, orow, r0, crow, l.s_row);
@@ -246,17 +262,8 @@ __device__ __forceinline__ void fmt_dual(const uint4 (&v)[kTileChunks], TileLds&
   __syncthreads();
   const int t = threadIdx.x;
   if (t < kTR) fmt_scales<F>(l.s_row, t, rows_valid, cols_valid, orow, r0, crow);
-  else fmt_scales<F>(l.s_col, t - kTR, cols_valid, rows_pad, ocol, crow, r0);
+  else if (t < kTR + kTC) fmt_scales<F>(l.s_col, t - kTR, cols_valid, rows_pad, ocol, crow, r0);
   if (more) __syncthreads();
-}
-
-// Row-wise codes only.
-template <class F, bool FULL>
-__device__ __forceinline__ void fmt_row(const uint4 (&v)[kTileChunks], uint32_t* s_row, int rows_valid, int cols_valid,
-                                        const TileOut& orow, int64_t r0, int64_t crow) {
-  fmt_rowq<F, FULL>(v, rows_valid, cols_valid, orow, r0, crow, s_row);
-  __syncthreads();
-  if ((int)threadIdx.x < kTR) fmt_scales<F>(s_row, threadIdx.x, rows_valid, cols_valid, orow, r0, crow);
 }
 
 // Quantizes one chunk of row `row` at column `col` (a multiple of 8) and

@@ -558,14 +558,14 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
   constexpr int kB = F32 ? 4 : 2;
   const uint32_t t = threadIdx.x, cc = t & 15, tr = t >> 4;
   const char* base = static_cast<const char*>(a.x) + (r0 * a.ld + c0) * kB;
-  RawChunk<F32> raw[kTileChunks];
+  RawChunk<F32> raw[kChunks];
 #pragma unroll
-  for (int j = 0; j < kTileChunks; ++j) {
+  for (int j = 0; j < kChunks; ++j) {
     if constexpr (FULL) {
-      __builtin_memcpy(&raw[j], base + (int64_t)(16 * j) * a.ld * kB + (tr * (uint32_t)a.ld + cc * 8) * kB, sizeof(raw[j]));
+      __builtin_memcpy(&raw[j], base + (int64_t)(kRowStep * j) * a.ld * kB + (tr * (uint32_t)a.ld + cc * 8) * kB, sizeof(raw[j]));
     } else {
       float f[8];
-      const int row = tr + 16 * j;
+      const int row = tr + kRowStep * j;
       if (row < rows_valid && (int)cc * 8 < cols_valid)
         load_logits<F32>(base + row * a.ld * kB, cc * 8, cols_valid, -INFINITY, f);
       else
@@ -592,10 +592,10 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
     rows[t] = g;
   }
   __syncthreads();
-  uint4 v[kTileChunks];
+  uint4 v[kChunks];
 #pragma unroll
-  for (int j = 0; j < kTileChunks; ++j) {
-    const GradRow g = rows[tr + 16 * j];
+  for (int j = 0; j < kChunks; ++j) {
+    const GradRow g = rows[tr + kRowStep * j];
     float f[8];
     if constexpr (F32) __builtin_memcpy(f, &raw[j], 32);
     else unpack8(raw[j].w[0], f);
@@ -613,7 +613,7 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
     }
     v[j] = pack8(f);
     if constexpr (!FULL) {   // rows and columns that only fill up: +0
-      const int left = (int)(tr + 16 * j) < rows_valid ? cols_valid - (int)cc * 8 : 0;
+      const int left = (int)(tr + kRowStep * j) < rows_valid ? cols_valid - (int)cc * 8 : 0;
       uint32_t* w = reinterpret_cast<uint32_t*>(&v[j]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = left >= 2 * k + 2 ? w[k] : left == 2 * k + 1 ? w[k] & 0xFFFFu : 0u;
@@ -624,7 +624,7 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
 }
 
 template <class F, bool F32>
-__global__ __launch_bounds__(kTileThreads) void k_logprob_bwd(LogprobArgs a) {
+__global__ __launch_bounds__(kFmtThreads) void k_logprob_bwd(LogprobArgs a) {
   __shared__ TileLds l;
   __shared__ GradRow rows[kTR];
   const int64_t r0 = (int64_t)blockIdx.y * kTR;
@@ -673,8 +673,8 @@ hipError_t launch_logprob_fwd(const LogprobArgs& a, hipStream_t s) {
 hipError_t launch_logprob_bwd(const LogprobArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.vocab_pad + kTC - 1) / kTC), (unsigned)((a.rows_pad + kTR - 1) / kTR));
   with_fmt(a.rceil, a.k128, [&](auto f) {
-    if (a.f32) hipLaunchKernelGGL((k_logprob_bwd<decltype(f), true>), grid, dim3(kTileThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_logprob_bwd<decltype(f), false>), grid, dim3(kTileThreads), 0, s, a);
+    if (a.f32) hipLaunchKernelGGL((k_logprob_bwd<decltype(f), true>), grid, dim3(kFmtThreads), 0, s, a);
+    else hipLaunchKernelGGL((k_logprob_bwd<decltype(f), false>), grid, dim3(kFmtThreads), 0, s, a);
   });
   return hipGetLastError();
 }

@@ -245,15 +245,15 @@ struct NormTailArgs {
 template <class F, bool NORM, bool FULL>
 __device__ __forceinline__ void norm_col_tile(const NormTailArgs& a, TileLds& l, int64_t r0, int64_t c0, int rows_valid,
                                               int rows_pad, int cols_valid) {
-  uint4 v[kTileChunks];
+  uint4 v[kChunks];
   fmt_load<FULL>(v, a.x + r0 * a.ld + c0, a.ld, rows_valid, cols_valid);
   const int t = threadIdx.x, cc = t & 15;
   if constexpr (NORM) {
     float w[8] = {};
     if (FULL || cc * 8 < cols_valid) load8f(a.w + c0 + cc * 8, w);
 #pragma unroll
-    for (int j = 0; j < kTileChunks; ++j) {
-      const int row = (t >> 4) + 16 * j;
+    for (int j = 0; j < kChunks; ++j) {
+      const int row = (t >> 4) + kRowStep * j;
       // rows past the last stay +0 whatever w holds
       if (FULL || row < rows_valid) v[j] = norm_chunk(v[j], a.rstd[r0 + row], w);
     }
@@ -266,7 +266,7 @@ __device__ __forceinline__ void norm_col_tile(const NormTailArgs& a, TileLds& l,
   if (t < kTC) fmt_scales<F>(l.s_col, t, cols_valid, rows_pad, o, c0, r0);
 }
 
-// dw[c] = sum over the parts of work[part, c]: 32 columns per workgroup, 32
+// dw[c] = sum over the parts of work[part, c]: 32 columns per workgroup, 64
 // threads down each group of 4, joined in LDS in a fixed order.
 __device__ __forceinline__ void join_dw(const NormTailArgs& a, float4* acc) {
   const int c = threadIdx.x & 7, p0 = threadIdx.x >> 3;
@@ -275,24 +275,24 @@ __device__ __forceinline__ void join_dw(const NormTailArgs& a, float4* acc) {
   auto add = [](float4 u, float4 v) { return make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w); };
   float4 s0 = make_float4(0, 0, 0, 0), s1 = s0, s2 = s0, s3 = s0;
   int64_t p = p0;
-  for (; p + 96 < a.parts; p += 128) {
+  for (; p + 192 < a.parts; p += 256) {
     s0 = add(s0, src[p * ld]);
-    s1 = add(s1, src[(p + 32) * ld]);
-    s2 = add(s2, src[(p + 64) * ld]);
-    s3 = add(s3, src[(p + 96) * ld]);
+    s1 = add(s1, src[(p + 64) * ld]);
+    s2 = add(s2, src[(p + 128) * ld]);
+    s3 = add(s3, src[(p + 192) * ld]);
   }
-  for (; p < a.parts; p += 32) s0 = add(s0, src[p * ld]);
+  for (; p < a.parts; p += 64) s0 = add(s0, src[p * ld]);
   acc[threadIdx.x] = add(add(s0, s1), add(s2, s3));
   __syncthreads();
   if (p0 == 0) {
     float4 t = make_float4(0, 0, 0, 0);
-    for (int i = 0; i < 32; ++i) t = add(t, acc[8 * i + c]);
+    for (int i = 0; i < 64; ++i) t = add(t, acc[8 * i + c]);
     reinterpret_cast<float4*>(a.dw + (int64_t)blockIdx.x * 32)[c] = t;
   }
 }
 
 template <class F, bool NORM>
-__global__ __launch_bounds__(kTileThreads) void k_norm_tail(NormTailArgs a) {
+__global__ __launch_bounds__(kFmtThreads) void k_norm_tail(NormTailArgs a) {
   __shared__ TileLds l;
   if ((int)blockIdx.x < a.dw_blocks) {
     join_dw(a, reinterpret_cast<float4*>(l.v));
@@ -318,7 +318,7 @@ static hipError_t launch_tail(const NormTailArgs& c, bool rceil, bool k128, hipS
   const int64_t tiles = c.q ? (c.cols + kTC - 1) / kTC * ((c.rows_pad + kTR - 1) / kTR) : 0;
   const dim3 grid((unsigned)(c.dw_blocks + tiles));
   with_fmt(rceil, k128, [&](auto f) {
-    hipLaunchKernelGGL((k_norm_tail<decltype(f), NORM>), grid, dim3(kTileThreads), 0, s, c);
+    hipLaunchKernelGGL((k_norm_tail<decltype(f), NORM>), grid, dim3(kFmtThreads), 0, s, c);
   });
   return hipGetLastError();
 }

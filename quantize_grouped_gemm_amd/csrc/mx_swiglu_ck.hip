@@ -20,24 +20,24 @@ namespace mxk {
 template <class F, bool FULL>
 __device__ __forceinline__ void swiglu_ck_fwd_tile(const SwigluCkArgs& a, TileLds& l, uint32_t (&s_ck)[2][kTR], int64_t r0,
                                                    int64_t c0, int rows_valid, int rows_pad, int cols_valid) {
-  uint4 v[kTileChunks], w[kTileChunks];
+  uint4 v[kChunks], w[kChunks];
   fmt_load<FULL>(v, a.a + r0 * a.ld_ab + c0, a.ld_ab, rows_valid, cols_valid);
   fmt_load<FULL>(w, a.b + r0 * a.ld_ab + c0, a.ld_ab, rows_valid, cols_valid);
   const TileOut ock{a.q_ck, a.s_ck, 2 * a.hidden, a.rows, F::k128};
   fmt_rowq<F, FULL>(v, rows_valid, cols_valid, ock, r0, c0, s_ck[0]);
   fmt_rowq<F, FULL>(w, rows_valid, cols_valid, ock, r0, a.hidden + c0, s_ck[1]);
 #pragma unroll
-  for (int j = 0; j < kTileChunks; ++j)
+  for (int j = 0; j < kChunks; ++j)
     v[j] = make_uint4(swiglu_pair(v[j].x, w[j].x), swiglu_pair(v[j].y, w[j].y),
                       swiglu_pair(v[j].z, w[j].z), swiglu_pair(v[j].w, w[j].w));
   fmt_dual<F, FULL>(v, l, rows_valid, rows_pad, cols_valid, TileOut{a.q_row, a.s_row, a.hidden, a.rows, F::k128},
                     TileOut{a.q_col, a.s_col, a.rows_pad, a.hidden, F::k128}, r0, c0, false);
-  const int t = threadIdx.x & (kTR - 1), half = threadIdx.x / kTR;
-  fmt_scales<F>(s_ck[half], t, rows_valid, cols_valid, ock, r0, half * a.hidden + c0);
+  const int t = threadIdx.x & (kTR - 1), half = (int)threadIdx.x / kTR - 2;   // the threads that fmt_dual leaves idle
+  if (half >= 0) fmt_scales<F>(s_ck[half], t, rows_valid, cols_valid, ock, r0, half * a.hidden + c0);
 }
 
 template <class F>
-__global__ __launch_bounds__(kTileThreads) void k_swiglu_ck_fwd(SwigluCkArgs a) {
+__global__ __launch_bounds__(kFmtThreads) void k_swiglu_ck_fwd(SwigluCkArgs a) {
   __shared__ TileLds l;
   __shared__ uint32_t s_ck[2][kTR];
   const int64_t r0 = (int64_t)blockIdx.y * kTR;
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(kTileThreads) void k_swiglu_ck_fwd(SwigluCkArgs a) 
 // one, the compiler carried the widened float32 values of all chunks through
 // it, 256 VGPRs); the caller drops what comes of them.
 template <class F, bool FULL>
-__device__ __forceinline__ void tile_load_codes(uint2 (&q)[kTileChunks], uint32_t (&sb)[kTileChunks], const uint8_t* qp,
+__device__ __forceinline__ void tile_load_codes(uint2 (&q)[kChunks], uint32_t (&sb)[kChunks], const uint8_t* qp,
                                                 const uint8_t* sp, int64_t ld, int64_t rows, int64_t r0, int64_t c0,
                                                 int rows_valid, int cols_valid) {
   const uint32_t t = threadIdx.x;
@@ -66,11 +66,11 @@ __device__ __forceinline__ void tile_load_codes(uint2 (&q)[kTileChunks], uint32_
   const uint8_t* sbase = sp + (F::k128 ? ((c0 >> 7) * rows + r0) * 4 : r0 * (ld / kBlock) + (c0 >> 5));
   const uint32_t sld = F::k128 ? 4u : (uint32_t)(ld / kBlock);
 #pragma unroll
-  for (int j = 0; j < kTileChunks; ++j) {
-    const uint32_t r = FULL ? (t >> 4) + 16 * j : (uint32_t)min((int)(t >> 4) + 16 * j, rows_valid - 1);
+  for (int j = 0; j < kChunks; ++j) {
+    const uint32_t r = FULL ? (t >> 4) + kRowStep * j : (uint32_t)min((int)(t >> 4) + kRowStep * j, rows_valid - 1);
     if constexpr (FULL) {
-      q[j] = *reinterpret_cast<const uint2*>(qbase + (int64_t)(16 * j) * ld + ((t >> 4) * (uint32_t)ld + c));
-      sb[j] = sbase[(int64_t)(16 * j) * sld + ((t >> 4) * sld + (c >> 5))];
+      q[j] = *reinterpret_cast<const uint2*>(qbase + (int64_t)(kRowStep * j) * ld + ((t >> 4) * (uint32_t)ld + c));
+      sb[j] = sbase[(int64_t)(kRowStep * j) * sld + ((t >> 4) * sld + (c >> 5))];
     } else {
       q[j] = *reinterpret_cast<const uint2*>(qbase + r * ld + c);
       sb[j] = sbase[(int64_t)r * sld + (c >> 5)];
@@ -82,15 +82,15 @@ template <class F, bool FULL>
 __device__ __forceinline__ void swiglu_ck_bwd_tile(const SwigluCkArgs& a, TileLds& l, int64_t r0, int64_t c0,
                                                    int rows_valid, int rows_pad, int cols_valid) {
   const int64_t H2 = 2 * a.hidden;
-  uint4 da[kTileChunks], db[kTileChunks];
+  uint4 da[kChunks], db[kChunks];
   {
-    uint2 qa[kTileChunks], qb[kTileChunks];
-    uint32_t sa[kTileChunks], sb[kTileChunks];
+    uint2 qa[kChunks], qb[kChunks];
+    uint32_t sa[kChunks], sb[kChunks];
     fmt_load<FULL>(da, a.dh + r0 * a.ld_dh + c0, a.ld_dh, rows_valid, cols_valid);
     tile_load_codes<F, FULL>(qa, sa, a.q_ck, a.s_ck, H2, a.rows, r0, c0, rows_valid, cols_valid);
     tile_load_codes<F, FULL>(qb, sb, a.q_ck, a.s_ck, H2, a.rows, r0, a.hidden + c0, rows_valid, cols_valid);
 #pragma unroll
-    for (int j = 0; j < kTileChunks; ++j) {
+    for (int j = 0; j < kChunks; ++j) {
       // one chunk's 32 float32 values at a time: left to itself the compiler
       // widens all eight chunks first
       asm volatile("" : "+v"(qa[j].x), "+v"(qa[j].y), "+v"(qb[j].x), "+v"(qb[j].y));
@@ -101,7 +101,7 @@ __device__ __forceinline__ void swiglu_ck_bwd_tile(const SwigluCkArgs& a, TileLd
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         swiglu_grad_f32(i & 1 ? bf16_hi(wd[i >> 1]) : bf16_lo(wd[i >> 1]), fa[i], fb[i], ga[i], gb[i]);
-      const bool ok = FULL || ((int)(threadIdx.x >> 4) + 16 * j < rows_valid && (int)(threadIdx.x & 15) * 8 < cols_valid);
+      const bool ok = FULL || ((int)(threadIdx.x >> 4) + kRowStep * j < rows_valid && (int)(threadIdx.x & 15) * 8 < cols_valid);
       da[j] = ok ? pack8(ga) : make_uint4(0, 0, 0, 0);
       db[j] = ok ? pack8(gb) : make_uint4(0, 0, 0, 0);
       asm volatile("" : "+v"(da[j].x), "+v"(da[j].y), "+v"(da[j].z), "+v"(da[j].w), "+v"(db[j].x), "+v"(db[j].y),
@@ -115,7 +115,7 @@ __device__ __forceinline__ void swiglu_ck_bwd_tile(const SwigluCkArgs& a, TileLd
 }
 
 template <class F>
-__global__ __launch_bounds__(kTileThreads, 4) void k_swiglu_ck_bwd(SwigluCkArgs a) {
+__global__ __launch_bounds__(kFmtThreads, 8) void k_swiglu_ck_bwd(SwigluCkArgs a) {
   __shared__ TileLds l;
   const int64_t r0 = (int64_t)blockIdx.y * kTR;
   const int64_t c0 = (int64_t)blockIdx.x * kTC;
@@ -134,14 +134,14 @@ static dim3 tile_grid(const SwigluCkArgs& a) {
 
 hipError_t launch_swiglu_ck_fwd(const SwigluCkArgs& a, hipStream_t s) {
   with_fmt(a.rceil, a.k128, [&](auto f) {
-    hipLaunchKernelGGL(k_swiglu_ck_fwd<decltype(f)>, tile_grid(a), dim3(kTileThreads), 0, s, a);
+    hipLaunchKernelGGL(k_swiglu_ck_fwd<decltype(f)>, tile_grid(a), dim3(kFmtThreads), 0, s, a);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_swiglu_ck_bwd(const SwigluCkArgs& a, hipStream_t s) {
   with_fmt(a.rceil, a.k128, [&](auto f) {
-    hipLaunchKernelGGL(k_swiglu_ck_bwd<decltype(f)>, tile_grid(a), dim3(kTileThreads), 0, s, a);
+    hipLaunchKernelGGL(k_swiglu_ck_bwd<decltype(f)>, tile_grid(a), dim3(kFmtThreads), 0, s, a);
   });
   return hipGetLastError();
 }
