@@ -19,7 +19,8 @@
  * T_pad, the next multiple of the layout's step (128 for MX_SCALES_K128, 32
  * for MX_SCALES_PLAIN): q_col [cols, T_pad], s_col the scales of that matrix.
  * They are then operands of mx_scaled_mm with K = T_pad. Row strides are at
- * most 2^26 elements where nothing else is stated.
+ * most 2^26 elements where nothing else is stated, and a tensor that is
+ * quantized has at most 2^21 tiles of 128 x 128 (2^35 elements).
  *
  * "MX(v)" below is the quantization of mx_quantize in the call's mode and
  * layout, applied to a bf16 matrix.

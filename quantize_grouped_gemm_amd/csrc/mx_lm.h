@@ -39,6 +39,7 @@ struct SwigluCkArgs {
   int64_t rows, hidden, rows_pad;
   bool rceil, k128;
   uint8_t *q_row, *s_row, *q_col, *s_col, *q_ck, *s_ck;
+  bool bands;                // order of the tiles, set by the launcher
 };
 
 struct LogprobArgs {
@@ -59,6 +60,7 @@ struct LogprobArgs {
   int64_t vocab_pad, rows_pad;
   bool rceil, k128;
   uint8_t *q_row, *s_row, *q_col, *s_col;
+  bool bands;                // order of the tiles, set by the launcher
 };
 
 constexpr int64_t kNormMaxCols = 16384;

@@ -20,6 +20,11 @@ constexpr int64_t kMaxRows = (int64_t)65535 * 128;   // one grid row per 128 tok
 // 32-bit byte offsets.
 constexpr int64_t kMaxStride = 1ll << 26;
 
+// One workgroup of 512 threads per 128 x 128 tile; a grid holds 2^32 threads.
+constexpr int64_t kMaxTiles = 1ll << 21;
+
+bool tiles_fit(int64_t rows, int64_t cols) { return (rows + 127) / 128 * ((cols + 127) / 128) <= kMaxTiles; }
+
 bool al8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 int64_t step_of(mx_scale_layout layout) { return layout == MX_SCALES_K128 ? 128 : 32; }
 int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
@@ -37,6 +42,7 @@ mx_status check_extent(const char* fn, int64_t rows, int64_t cols, mx_scale_layo
   MX_REQUIRE(cols > 0 && cols <= max_cols && cols % m == 0, MX_ERR_SHAPE,
              "%s: the row length (%lld) must be a positive multiple of %lld, at most %lld", fn, (long long)cols,
              (long long)m, (long long)max_cols);
+  MX_REQUIRE(tiles_fit(rows, cols), MX_ERR_SHAPE, "%s: too many tiles for one launch", fn);
   return MX_OK;
 }
 
@@ -237,6 +243,7 @@ mx_status mx_token_logprobs_bwd(const void* x, mx_dtype x_dtype, int64_t ld, int
   MX_CHECK(check_format(fn, mode, layout));
   MX_CHECK(check_logits(fn, x, x_dtype, ld, rows, vocab, scale));
   MX_REQUIRE(vocab <= kMaxStride - 128 && ld <= kMaxStride, MX_ERR_SHAPE, "%s: vocab or ld above 2^26", fn);
+  MX_REQUIRE(tiles_fit(rows, vocab), MX_ERR_SHAPE, "%s: too many tiles for one launch", fn);
   if (rows == 0) return MX_OK;
   MX_REQUIRE(targets && stats && entropy, MX_ERR_NULL, "%s: targets/stats/entropy NULL", fn);
   MX_REQUIRE(al8(targets) && al8(stats) && al4(entropy) && al4(dlogp) && al4(dent) && al4(dev_err), MX_ERR_ALIGN,

@@ -581,7 +581,7 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
       const int64_t row = r0 + t;
       const float m = a.stats[2 * row], ls = a.stats[2 * row + 1];
       const int64_t tg = row_target(a, row);
-      if (blockIdx.x == 0 && a.dev_err && tg < 0 && a.targets[row] != a.ignore_index) atomicOr(a.dev_err, 8);
+      if (c0 == 0 && a.dev_err && tg < 0 && a.targets[row] != a.ignore_index) atomicOr(a.dev_err, 8);
       if (!(m == -INFINITY && ls == -INFINITY)) {   // a row with nothing left has gradient 0
         const float d = tg >= 0 && a.dlogp ? a.dlogp[row] : 0.0f;
         const float dent = a.dent ? a.dent[row] : 0.0f;
@@ -627,8 +627,9 @@ template <class F, bool F32>
 __global__ __launch_bounds__(kFmtThreads) void k_logprob_bwd(LogprobArgs a) {
   __shared__ TileLds l;
   __shared__ GradRow rows[kTR];
-  const int64_t r0 = (int64_t)blockIdx.y * kTR;
-  const int64_t c0 = (int64_t)blockIdx.x * kTC;
+  const TilePos at = tile_pos(blockIdx.x, (uint32_t)((a.vocab_pad + kTC - 1) / kTC), (uint32_t)((a.rows_pad + kTR - 1) / kTR),
+                              a.bands);
+  const int64_t r0 = at.r0, c0 = at.c0;
   const int rows_valid = (int)min<int64_t>(kTR, a.rows - r0);
   const int rows_pad = (int)min<int64_t>(kTR, a.rows_pad - r0);
   const int cols_valid = (int)min<int64_t>(kTC, a.vocab - c0);
@@ -670,8 +671,22 @@ hipError_t launch_logprob_fwd(const LogprobArgs& a, hipStream_t s) {
   return a.top ? launch_fwd<false, true>(a, s) : launch_fwd<false, false>(a, s);
 }
 
-hipError_t launch_logprob_bwd(const LogprobArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.vocab_pad + kTC - 1) / kTC), (unsigned)((a.rows_pad + kTR - 1) / kTR));
+// Bands (tile_pos) for large gradients whose rows are aligned: their pitch
+// sends the 128 rows of a tile to few memory channels at a time, and eight
+// bands spread that. 4096 x 131072 498 -> 452 us, 8192 x 65536 490 -> 436,
+// 4096 x 50304 float32 265 -> 248; without it smaller gradients are faster
+// (8192 x 16384 116 against 132 us, 2048 x 131072 float32 310 against 327), and
+// so are unaligned rows (6000 x 100001 489 against 528).
+static bool grad_bands(const LogprobArgs& a, int64_t nx, int64_t ny) {
+  const int64_t pitch = a.ld * (a.f32 ? 4 : 2);
+  return nx * ny >= 48 * 256 && ny >= 32 && pitch % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
+}
+
+hipError_t launch_logprob_bwd(const LogprobArgs& args, hipStream_t s) {
+  LogprobArgs a = args;
+  const int64_t nx = (a.vocab_pad + kTC - 1) / kTC, ny = (a.rows_pad + kTR - 1) / kTR;
+  a.bands = grad_bands(a, nx, ny);
+  const dim3 grid((unsigned)(nx * ny));
   with_fmt(a.rceil, a.k128, [&](auto f) {
     if (a.f32) hipLaunchKernelGGL((k_logprob_bwd<decltype(f), true>), grid, dim3(kFmtThreads), 0, s, a);
     else hipLaunchKernelGGL((k_logprob_bwd<decltype(f), false>), grid, dim3(kFmtThreads), 0, s, a);

@@ -196,3 +196,22 @@ def test_strided_and_unaligned_rows(gpu):
     gb = lm.token_logprobs_bwd(v.contiguous(), t, a["stats"], a["entropy"], dlogp=torch.ones(19, device=dev()))
     for k in ga:
         assert torch.equal(ga[k], gb[k]), k
+
+
+def test_bwd_tile_orders_agree(gpu):
+    """A large aligned gradient walks its tiles in another order: the same
+    bytes as from calls over 2048 of its rows."""
+    T, V = 4100, 49152
+    g = torch.Generator(device=dev()).manual_seed(0)
+    x = (torch.randn((T, V), generator=g, device=dev()) * 2.5).to(BF)
+    t = torch.randint(0, V, (T,), generator=g, device=dev())
+    f = lm.token_logprobs(x, t)
+    dl, de = torch.randn(T, generator=g, device=dev()) / T, torch.randn(T, generator=g, device=dev()) / T
+    out = lm.token_logprobs_bwd(x, t, f["stats"], f["entropy"], dl, de)
+    for r0 in range(0, T, 2048):
+        r = slice(r0, min(r0 + 2048, T))
+        part = lm.token_logprobs_bwd(x[r], t[r], f["stats"][r], f["entropy"][r], dl[r], de[r])
+        n = part["q_col"].shape[1]
+        assert torch.equal(out["q_row"][r], part["q_row"]) and torch.equal(out["s_row"][:, r], part["s_row"])
+        assert torch.equal(out["q_col"][:, r0:r0 + n], part["q_col"])
+        assert torch.equal(out["s_col"][r0 // 128:(r0 + n) // 128], part["s_col"])

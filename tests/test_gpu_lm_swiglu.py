@@ -59,6 +59,31 @@ def test_agrees_with_the_bf16_operators(gpu, T, H):
         assert torch.equal(got[k], ref[k]), k
 
 
+@pytest.mark.parametrize("T,H,layout", [(8192, 384, "k128"), (8200, 160, "plain"), (9001, 128, "k128")])
+def test_tile_orders_agree(gpu, T, H, layout):
+    """From 8192 rows on the tiles are walked in another order: the same bytes
+    as from shorter calls over the same rows (multiples of the block step)."""
+    z, a, b = _z(T, H, 17, 0)
+    dh = synth.normal_bf16((T, H), 1e-2, synth.generator(18)).to(dev())
+    out = lm.swiglu_ckpt_fwd(a, b, layout=layout)
+    got = lm.swiglu_ckpt_bwd(dh, out["q_ck"], out["s_ck"], layout=layout)
+    for r0 in range(0, T, 4096):
+        r1 = min(r0 + 4096, T)
+        part = lm.swiglu_ckpt_fwd(a[r0:r1], b[r0:r1], layout=layout)
+        pb = lm.swiglu_ckpt_bwd(dh[r0:r1], part["q_ck"], part["s_ck"], layout=layout)
+        cols = slice(r0, r0 + lm.padded_rows(r1 - r0, layout))
+        for whole, piece, keys in ((out, part, ("row", "ck")), (got, pb, ("row",))):
+            for k in keys:
+                assert torch.equal(whole["q_" + k][r0:r1], piece["q_" + k]), (k, r0)
+            assert torch.equal(whole["q_col"][:, cols], piece["q_col"]), r0
+            if layout == "plain":
+                assert torch.equal(whole["s_row"][r0:r1], piece["s_row"])
+                assert torch.equal(whole["s_col"][:, cols.start // 32:cols.stop // 32], piece["s_col"])
+            else:
+                assert torch.equal(whole["s_row"][:, r0:r1], piece["s_row"])
+                assert torch.equal(whole["s_col"][cols.start // 128:cols.stop // 128], piece["s_col"])
+
+
 def test_special_values(gpu):
     """Zero halves give zeros, a NaN block stays a NaN block and reaches only
     its own gradients, every scale byte is read back."""

@@ -175,6 +175,13 @@ def test_abi_refusals():
     assert fwd(x=odd) == 3 and fwd(ld=64) == 3 and fwd(ld=132) == 3 and fwd(w=odd) == 3 and fwd(s=odd) == 3
     assert fwd(rows=0) == 0
 
+    # more than 2^21 tiles, row strides above 2^26
+    assert fwd(rows=65535 * 128, cols=16384, ld=16384) == 2 and b"tiles" in L.mx_last_error()
+    assert fwd(ld=(1 << 26) + 8) == 2
+    assert L.mx_token_logprobs_bwd(p, 0, 1 << 26, 4, 1 << 26, p, -100, p, p, p, p, 1.0, 0, 1, p, p, p, p, None, None) == 2
+    assert L.mx_token_logprobs_bwd(p, 0, 1 << 20, 1 << 20, 1 << 20, p, -100, p, p, p, p, 1.0, 0, 1, p, p, p, p, None,
+                                   None) == 2
+
     def bwd(x=p, qk=None, sk=None, dw=p, work=p, dx=p, cols=128, rows=4):
         return L.mx_add_rmsnorm_bwd(p, 128, p, p, x, 128, qk, sk, None, 0, rows, cols, 0, 1, dx, dw, p, p, None, None,
                                     work, None)
