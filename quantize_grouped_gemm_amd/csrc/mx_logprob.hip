@@ -143,9 +143,22 @@ __device__ __forceinline__ float max_of(const float (&f)[N], float m) {
   return m;
 }
 
+// How many of n keys in LDS are larger than `key`. Unrolled: one read in flight
+// at a time would pay LDS's latency for each.
+__device__ __forceinline__ int count_larger(const uint64_t* keys, int n, uint64_t key) {
+  int r = 0, j = 0;
+  for (; j + 8 <= n; j += 8) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) r += keys[j + u] > key ? 1 : 0;
+  }
+  for (; j < n; ++j) r += keys[j] > key ? 1 : 0;
+  return r;
+}
+
 struct TopLds {
   uint16_t slot[kSlots][kThreads];
   uint64_t cand[kCand];
+  uint64_t best[kMaxTop];
   uint64_t thr;          // entries with a larger key are candidates
   uint16_t list[kList];
   int count, hits;
@@ -156,32 +169,22 @@ struct TopLds {
 // unique, so an entry's rank is the number of larger ones. All threads call
 // it; barriers inside, the last one after the writes.
 __device__ __forceinline__ void keep_top(TopLds& l, int top) {
-  constexpr int kPer = (kCand + kThreads - 1) / kThreads;
   const int t = threadIdx.x;
   __syncthreads();
   const int n = l.count;
-  uint64_t key[kPer];
-  int rank[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int at = t + kThreads * i;
-    rank[i] = top;
-    if (at < n) {
-      key[i] = l.cand[at];
-      int r = 0;
-      for (int j = 0; j < n; ++j) r += l.cand[j] > key[i] ? 1 : 0;
-      rank[i] = r;
-    }
+#pragma unroll 1
+  for (int i = t; i < n; i += kThreads) {
+    const uint64_t key = l.cand[i];
+    const int r = count_larger(l.cand, n, key);
+    if (r < top) l.best[r] = key;
   }
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (rank[i] < top) {
-      l.cand[rank[i]] = key[i];
-      if (rank[i] == top - 1) l.thr = key[i];
-    }
+  const int kept = min(n, top);
+  if (t < kept) l.cand[t] = l.best[t];
+  if (t == 0) {
+    l.count = kept;
+    if (kept == top) l.thr = l.best[top - 1];
   }
-  if (t == 0) l.count = min(n, top);
   __syncthreads();
 }
 
@@ -510,15 +513,11 @@ __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobArgs a, Split 
     const RowOut o = join_row<F32>(a, row, v, c);
     const int lead = min((2 * a.top + sp.parts - 1) / sp.parts, a.top);
     const int leads = lead * sp.parts;   // at most 2 top + parts
-    const int at = t < leads ? (t / lead) * a.top + t % lead : 0;
     __syncthreads();
-    if (t < leads) {
-      const uint64_t k = keys[at];
-      int r = 0;
-      for (int i = 0; i < sp.parts; ++i)
-        for (int j = 0; j < lead; ++j) r += keys[i * a.top + j] > k ? 1 : 0;
-      if (r == a.top - 1 && k) bound = k;
-    }
+    uint64_t k0 = 0;
+    if (t < leads) cand[t] = k0 = keys[(t / lead) * a.top + t % lead];
+    __syncthreads();
+    if (t < leads && k0 && count_larger(cand, leads, k0) == a.top - 1) bound = k0;
     __syncthreads();
     const uint64_t b = bound;
     for (int i = t; i < total; i += kThreads) {
@@ -529,8 +528,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobArgs a, Split 
     const int n = count;
     for (int i = t; i < n; i += kThreads) {
       const uint64_t k = cand[i];
-      int r = 0;
-      for (int j = 0; j < n; ++j) r += cand[j] > k ? 1 : 0;
+      const int r = count_larger(cand, n, k);
       if (r < a.top) best[r] = k;
     }
     __syncthreads();

@@ -19,7 +19,7 @@ import ctypes
 import torch
 
 from . import mx
-from .mx import MXError, _check, _device, _flag, _ptr, _stream, _u8, _want, _want_rows, scale_shape
+from .mx import MXError, _check, _flag, _want, _want_rows, scale_shape
 
 IGNORE_INDEX = -100
 MAX_COLS = 16384      # longest row of the norm
@@ -60,49 +60,92 @@ def padded_rows(T, layout="k128"):
     return (T + step - 1) // step * step
 
 
+# The operators run for a few microseconds on small inputs, so the checks are
+# written to cost little where they pass: one comparison each, and the
+# functions of mx, which find out what is wrong, only where one fails.
+
+_U8, _BF, _F32, _I32T = torch.uint8, torch.bfloat16, torch.float32, torch.int32
+_empty = torch.empty
+
+
 def _format(mode, layout):
-    if mode not in mx._MODES:
-        raise MXError(f"mode: {mode!r}, expected 'rceil' or 'floor'")
-    if layout not in mx._LAYOUTS:
-        raise MXError(f"layout: {layout!r}, expected 'k128' or 'plain'")
-    return mx._MODES[mode], mx._LAYOUTS[layout]
+    try:
+        return mx._MODES[mode], mx._LAYOUTS[layout]
+    except (KeyError, TypeError):
+        if mode not in mx._MODES:
+            raise MXError(f"mode: {mode!r}, expected 'rceil' or 'floor'") from None
+        raise MXError(f"layout: {layout!r}, expected 'k128' or 'plain'") from None
 
 
-def _matrix(t, name, dtypes=(torch.bfloat16,)):
+def _matrix(t, name, dtypes=(_BF,)):
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in dtypes:
         raise MXError(f"{name}: expected a 2-D tensor of {', '.join(str(d) for d in dtypes)}")
     return t.shape
 
 
-def _ld(t):
-    """Row stride; that of a single row does not matter."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(t, name, dtype, shape):
+    """Checks a matrix of contiguous rows; returns its row stride (that of a
+    single row does not matter)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
+        _want_rows(t, name, dtype, shape)
+    ld, one = t.stride()
+    if one != 1 or ld < shape[1]:
+        _want_rows(t, name, dtype, shape)
+    return ld if shape[0] > 1 else shape[1]
 
 
-def _codes(out, keys, R, C, layout, dev):
-    """The codes [R, C] and scales under keys = ("q_..", "s_.."), taken from
-    `out` or allocated."""
-    q, s = keys
-    shape = scale_shape(R, C, layout)
+def _whole(t, name, dtype, shape):
+    """Checks a contiguous tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _want(t, name, dtype, shape=shape)
+
+
+def _out(out, key, shape, dtype, dev):
+    """The output under `key`, taken from `out` or allocated; its address."""
+    t = out.get(key)
+    if t is None:
+        t = out[key] = _empty(*shape, dtype=dtype, device=dev)
+    else:
+        _whole(t, key, dtype, shape)
+    return t.data_ptr()
+
+
+def _codes(out, q, s, R, C, layout, dev):
+    """The codes [R, C] and scales under the keys q and s; their addresses.
+    Given ones may have any shape of the right size."""
     if out.get(q) is None:
-        out[q] = _u8((R, C), dev)
+        out[q] = _empty(R, C, dtype=_U8, device=dev)
     else:
-        _want(out[q], q, torch.uint8, R * C)
+        _want(out[q], q, _U8, R * C)
     if out.get(s) is None:
-        out[s] = _u8(shape, dev)
+        if layout == "k128":
+            out[s] = _empty(C // 128, R, 4, dtype=_U8, device=dev)
+        else:
+            out[s] = _empty(R, C // 32, dtype=_U8, device=dev)
     else:
-        _want(out[s], s, torch.uint8, R * C // 32)
+        _want(out[s], s, _U8, R * C // 32)
+    return out[q].data_ptr(), out[s].data_ptr()
 
 
-def _tensor(out, key, shape, dtype, dev):
-    if out.get(key) is None:
-        out[key] = torch.empty(shape, dtype=dtype, device=dev)
-    else:
-        _want(out[key], key, dtype, shape=shape)
-    return out[key]
+_NONE = (None, None)
 
 
-_ROW, _COL, _CK = ("q_row", "s_row"), ("q_col", "s_col"), ("q_ck", "s_ck")
+def _launch(name, given, tensors, args):
+    """Checks that every tensor is on the current device and calls the library
+    on torch's current stream. `given`: outputs that the caller passed."""
+    idx = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != idx:
+            mx._device(*tensors)
+    if given:
+        mx._device(tensors[0], *[t for t in given.values() if isinstance(t, torch.Tensor)])
+    if idx < 0 or idx != torch.cuda.current_device():
+        mx._device(*tensors)
+    _check(getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(idx)), name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _blocks(name, n, layout):
@@ -126,29 +169,19 @@ def add_rmsnorm_quant(x, w, r=None, eps=1e-6, mode="rceil", layout="k128", colwi
     q_col / s_col [C, padded_rows(T)], and with checkpoint q_ck / s_ck, the
     row-wise MXFP8 copy of s that add_rmsnorm_bwd takes in its place."""
     m, lay = _format(mode, layout)
-    T, C = _matrix(x, "x")
-    _want_rows(x, "x", torch.bfloat16, (T, C))
-    if r is not None:
-        _want_rows(r, "r", torch.bfloat16, (T, C))
-    _want(w, "w", torch.float32, shape=(C,))
+    T, C = shape = _matrix(x, "x")
+    ld = _rows(x, "x", _BF, shape)
+    ld_r = 0 if r is None else _rows(r, "r", _BF, shape)
+    _whole(w, "w", _F32, (C,))
     _norm_width(C, layout)
-    dev = x.device
-    out = dict(out or {})
-    if r is not None:
-        _tensor(out, "sum", (T, C), torch.bfloat16, dev)
-    _tensor(out, "rstd", (T,), torch.float32, dev)
-    _codes(out, _ROW, T, C, layout, dev)
-    if colwise:
-        _codes(out, _COL, C, padded_rows(T, layout), layout, dev)
-    if checkpoint:
-        _codes(out, _CK, T, C, layout, dev)
-    _device(x, w, r, *out.values())
-    col = (_ptr(out["q_col"]), _ptr(out["s_col"])) if colwise else (None, None)
-    ck = (_ptr(out["q_ck"]), _ptr(out["s_ck"])) if checkpoint else (None, None)
-    st = lib().mx_add_rmsnorm_quant(_ptr(x), _ld(x), _ptr(r), 0 if r is None else _ld(r), _ptr(w), T, C, eps, m, lay,
-                                    None if r is None else _ptr(out["sum"]), _ptr(out["rstd"]), _ptr(out["q_row"]),
-                                    _ptr(out["s_row"]), *col, *ck, _stream(dev))
-    _check(st, "mx_add_rmsnorm_quant")
+    given, out, dev = out, dict(out or {}), x.device
+    total = None if r is None else _out(out, "sum", shape, _BF, dev)
+    rstd = _out(out, "rstd", (T,), _F32, dev)
+    row = _codes(out, "q_row", "s_row", T, C, layout, dev)
+    col = _codes(out, "q_col", "s_col", C, padded_rows(T, layout), layout, dev) if colwise else _NONE
+    ck = _codes(out, "q_ck", "s_ck", T, C, layout, dev) if checkpoint else _NONE
+    _launch("mx_add_rmsnorm_quant", given, (x, w, r),
+            (x.data_ptr(), ld, _addr(r), ld_r, w.data_ptr(), T, C, eps, m, lay, total, rstd, *row, *col, *ck))
     return out
 
 
@@ -163,44 +196,36 @@ def add_rmsnorm_bwd(dy, w, rstd, x=None, checkpoint=None, dsum=None, mode="rceil
     colwise, q_col / s_col. work: optional float32 scratch of bwd_work(T, C)
     elements."""
     m, lay = _format(mode, layout)
-    T, C = _matrix(dy, "dy")
-    _want_rows(dy, "dy", torch.bfloat16, (T, C))
-    _want(w, "w", torch.float32, shape=(C,))
-    _want(rstd, "rstd", torch.float32, shape=(T,))
+    T, C = shape = _matrix(dy, "dy")
+    ld = _rows(dy, "dy", _BF, shape)
+    _whole(w, "w", _F32, (C,))
+    _whole(rstd, "rstd", _F32, (T,))
     _norm_width(C, layout)
     if (x is None) == (checkpoint is None):
         raise MXError("give exactly one of x and checkpoint")
-    q_ck = s_ck = None
+    ld_x, q_ck, s_ck = 0, None, None
     if x is not None:
-        _want_rows(x, "x", torch.bfloat16, (T, C))
+        ld_x = _rows(x, "x", _BF, shape)
     else:
         q_ck, s_ck = checkpoint
-        _want(q_ck, "q_ck", torch.uint8, shape=(T, C))
-        _want(s_ck, "s_ck", torch.uint8, shape=scale_shape(T, C, layout))
-    if dsum is not None:
-        _want_rows(dsum, "dsum", torch.bfloat16, (T, C))
-    dev = dy.device
-    out = dict(out or {})
-    _tensor(out, "dx", (T, C), torch.bfloat16, dev)
-    _tensor(out, "dw", (C,), torch.float32, dev)
-    if rowwise:
-        _codes(out, _ROW, T, C, layout, dev)
-    if colwise:
-        _codes(out, _COL, C, padded_rows(T, layout), layout, dev)
+        _whole(q_ck, "q_ck", _U8, shape)
+        _whole(s_ck, "s_ck", _U8, scale_shape(T, C, layout))
+    ld_s = 0 if dsum is None else _rows(dsum, "dsum", _BF, shape)
+    given, out, dev = out, dict(out or {}), dy.device
+    dx = _out(out, "dx", shape, _BF, dev)
+    dw = _out(out, "dw", (C,), _F32, dev)
+    row = _codes(out, "q_row", "s_row", T, C, layout, dev) if rowwise else _NONE
+    col = _codes(out, "q_col", "s_col", C, padded_rows(T, layout), layout, dev) if colwise else _NONE
     n = bwd_work(T, C)
     if work is None:
-        work = torch.empty((n,), dtype=torch.float32, device=dev)
+        work = _empty(n, dtype=_F32, device=dev)
     else:
-        _want(work, "work", torch.float32)
+        _want(work, "work", _F32)
         if work.numel() < n:
             raise MXError(f"work: {work.numel()} elements, needs {n}")
-    _device(dy, w, rstd, x, q_ck, s_ck, dsum, work, *out.values())
-    row = (_ptr(out["q_row"]), _ptr(out["s_row"])) if rowwise else (None, None)
-    col = (_ptr(out["q_col"]), _ptr(out["s_col"])) if colwise else (None, None)
-    st = lib().mx_add_rmsnorm_bwd(_ptr(dy), _ld(dy), _ptr(w), _ptr(rstd), _ptr(x), 0 if x is None else _ld(x),
-                                  _ptr(q_ck), _ptr(s_ck), _ptr(dsum), 0 if dsum is None else _ld(dsum), T, C, m, lay,
-                                  _ptr(out["dx"]), _ptr(out["dw"]), *row, *col, _ptr(work), _stream(dev))
-    _check(st, "mx_add_rmsnorm_bwd")
+    _launch("mx_add_rmsnorm_bwd", given, (dy, w, rstd, x, q_ck, s_ck, dsum, work),
+            (dy.data_ptr(), ld, w.data_ptr(), rstd.data_ptr(), _addr(x), ld_x, _addr(q_ck), _addr(s_ck), _addr(dsum),
+             ld_s, T, C, m, lay, dx, dw, *row, *col, work.data_ptr()))
     return out
 
 
@@ -215,22 +240,16 @@ def swiglu_ckpt_fwd(a, b, mode="rceil", layout="k128", out=None):
     q_ck / s_ck, the row-wise MXFP8 copy of [a | b] [T, 2H] that
     swiglu_ckpt_bwd takes: the bf16 input need not be kept."""
     m, lay = _format(mode, layout)
-    T, H = _matrix(a, "a")
-    _want_rows(a, "a", torch.bfloat16, (T, H))
-    _want_rows(b, "b", torch.bfloat16, (T, H))
-    if _ld(a) != _ld(b):
+    T, H = shape = _matrix(a, "a")
+    ld = _rows(a, "a", _BF, shape)
+    if _rows(b, "b", _BF, shape) != ld:
         raise MXError("a and b must share a row stride")
     _blocks("hidden", H, layout)
-    dev = a.device
-    out = dict(out or {})
-    _codes(out, _ROW, T, H, layout, dev)
-    _codes(out, _COL, H, padded_rows(T, layout), layout, dev)
-    _codes(out, _CK, T, 2 * H, layout, dev)
-    _device(a, b, *out.values())
-    st = lib().mx_swiglu_ckpt_fwd(_ptr(a), _ptr(b), _ld(a), T, H, m, lay, _ptr(out["q_row"]), _ptr(out["s_row"]),
-                                  _ptr(out["q_col"]), _ptr(out["s_col"]), _ptr(out["q_ck"]), _ptr(out["s_ck"]),
-                                  _stream(dev))
-    _check(st, "mx_swiglu_ckpt_fwd")
+    given, out, dev = out, dict(out or {}), a.device
+    row = _codes(out, "q_row", "s_row", T, H, layout, dev)
+    col = _codes(out, "q_col", "s_col", H, padded_rows(T, layout), layout, dev)
+    ck = _codes(out, "q_ck", "s_ck", T, 2 * H, layout, dev)
+    _launch("mx_swiglu_ckpt_fwd", given, (a, b), (a.data_ptr(), b.data_ptr(), ld, T, H, m, lay, *row, *col, *ck))
     return out
 
 
@@ -238,31 +257,28 @@ def swiglu_ckpt_bwd(dh, q_ck, s_ck, mode="rceil", layout="k128", out=None):
     """Gradient of swiglu_ckpt_fwd from its checkpoint: dh bf16 [T, H] gives
     [dA | dB] [T, 2H] as q_row / s_row and q_col / s_col."""
     m, lay = _format(mode, layout)
-    T, H = _matrix(dh, "dh")
-    _want_rows(dh, "dh", torch.bfloat16, (T, H))
+    T, H = shape = _matrix(dh, "dh")
+    ld = _rows(dh, "dh", _BF, shape)
     _blocks("hidden", H, layout)
-    _want(q_ck, "q_ck", torch.uint8, shape=(T, 2 * H))
-    _want(s_ck, "s_ck", torch.uint8, shape=scale_shape(T, 2 * H, layout))
-    dev = dh.device
-    out = dict(out or {})
-    _codes(out, _ROW, T, 2 * H, layout, dev)
-    _codes(out, _COL, 2 * H, padded_rows(T, layout), layout, dev)
-    _device(dh, q_ck, s_ck, *out.values())
-    st = lib().mx_swiglu_ckpt_bwd(_ptr(dh), _ld(dh), _ptr(q_ck), _ptr(s_ck), T, H, m, lay, _ptr(out["q_row"]),
-                                  _ptr(out["s_row"]), _ptr(out["q_col"]), _ptr(out["s_col"]), _stream(dev))
-    _check(st, "mx_swiglu_ckpt_bwd")
+    _whole(q_ck, "q_ck", _U8, (T, 2 * H))
+    _whole(s_ck, "s_ck", _U8, scale_shape(T, 2 * H, layout))
+    given, out, dev = out, dict(out or {}), dh.device
+    row = _codes(out, "q_row", "s_row", T, 2 * H, layout, dev)
+    col = _codes(out, "q_col", "s_col", 2 * H, padded_rows(T, layout), layout, dev)
+    _launch("mx_swiglu_ckpt_bwd", given, (dh, q_ck, s_ck),
+            (dh.data_ptr(), ld, q_ck.data_ptr(), s_ck.data_ptr(), T, H, m, lay, *row, *col))
     return out
 
 
 def _logits(x, targets, scale):
-    T, V = _matrix(x, "x", (torch.bfloat16, torch.float32))
-    _want_rows(x, "x", x.dtype, (T, V))
+    T, V = shape = _matrix(x, "x", (_BF, _F32))
+    ld = _rows(x, "x", x.dtype, shape)
     if V < 1:
         raise MXError("x: empty vocabulary")
-    _want(targets, "targets", torch.int64, shape=(T,))
+    _whole(targets, "targets", torch.int64, (T,))
     if not 1e-6 <= scale <= 1e6:
         raise MXError(f"scale: {scale}, expected a number in [1e-6, 1e6]")
-    return T, V
+    return T, V, ld
 
 
 def token_logprobs(x, targets, scale=1.0, top=0, ignore_index=IGNORE_INDEX, out=None, dev_err=None):
@@ -276,26 +292,19 @@ def token_logprobs(x, targets, scale=1.0, top=0, ignore_index=IGNORE_INDEX, out=
     descending order, ties to the lower index. Entries of -infinity are ruled
     out. dev_err: optional int32 device flag word; bit 3 reports a target
     outside the vocabulary (treated as not scored)."""
-    T, V = _logits(x, targets, scale)
+    T, V, ld = _logits(x, targets, scale)
     if not 0 <= top <= min(MAX_TOP, V):
         raise MXError(f"top: {top}, expected 0 to {min(MAX_TOP, V)}")
-    dev = x.device
-    out = dict(out or {})
-    f32 = torch.float32
-    _tensor(out, "logp", (T,), f32, dev)
-    _tensor(out, "entropy", (T,), f32, dev)
-    _tensor(out, "stats", (T, 2), f32, dev)
-    if top:
-        _tensor(out, "top_logp", (T, top), f32, dev)
-        _tensor(out, "top_idx", (T, top), torch.int32, dev)
+    given, out, dev = out, dict(out or {}), x.device
+    logp = _out(out, "logp", (T,), _F32, dev)
+    entropy = _out(out, "entropy", (T,), _F32, dev)
+    stats = _out(out, "stats", (T, 2), _F32, dev)
+    alt = (_out(out, "top_logp", (T, top), _F32, dev), _out(out, "top_idx", (T, top), _I32T, dev)) if top else _NONE
     n = lib().mx_token_logprobs_work(T, V, top)
-    work = _u8((n,), dev) if n else None
-    _device(x, targets, _flag(dev_err), *out.values())
-    alt = (_ptr(out["top_logp"]), _ptr(out["top_idx"])) if top else (None, None)
-    st = lib().mx_token_logprobs(_ptr(x), mx._DT[x.dtype], _ld(x), T, V, _ptr(targets), ignore_index, scale, top,
-                                 _ptr(out["logp"]), _ptr(out["entropy"]), _ptr(out["stats"]), *alt, _ptr(work),
-                                 _ptr(dev_err), _stream(dev))
-    _check(st, "mx_token_logprobs")
+    work = _empty(n, dtype=_U8, device=dev) if n else None
+    _launch("mx_token_logprobs", given, (x, targets, _flag(dev_err)),
+            (x.data_ptr(), mx._DT[x.dtype], ld, T, V, targets.data_ptr(), ignore_index, scale, top, logp, entropy, stats,
+             *alt, _addr(work), _addr(dev_err)))
     return out
 
 
@@ -308,21 +317,18 @@ def token_logprobs_bwd(x, targets, stats, entropy, dlogp=None, dent=None, scale=
     [T, V_pad] and q_col / s_col [V_pad, padded_rows(T)], with V_pad = V
     rounded up to the layout's block step (128 or 32) and zeros past V."""
     m, lay = _format(mode, layout)
-    T, V = _logits(x, targets, scale)
-    _want(stats, "stats", torch.float32, shape=(T, 2))
-    _want(entropy, "entropy", torch.float32, shape=(T,))
-    for t, name in ((dlogp, "dlogp"), (dent, "dent")):
-        if t is not None:
-            _want(t, name, torch.float32, shape=(T,))
-    dev = x.device
-    out = dict(out or {})
+    T, V, ld = _logits(x, targets, scale)
+    _whole(stats, "stats", _F32, (T, 2))
+    _whole(entropy, "entropy", _F32, (T,))
+    if dlogp is not None:
+        _whole(dlogp, "dlogp", _F32, (T,))
+    if dent is not None:
+        _whole(dent, "dent", _F32, (T,))
+    given, out, dev = out, dict(out or {}), x.device
     Vp = padded_rows(V, layout)
-    _codes(out, _ROW, T, Vp, layout, dev)
-    _codes(out, _COL, Vp, padded_rows(T, layout), layout, dev)
-    _device(x, targets, stats, entropy, dlogp, dent, _flag(dev_err), *out.values())
-    st = lib().mx_token_logprobs_bwd(_ptr(x), mx._DT[x.dtype], _ld(x), T, V, _ptr(targets), ignore_index, _ptr(stats),
-                                     _ptr(entropy), _ptr(dlogp), _ptr(dent), scale, m, lay, _ptr(out["q_row"]),
-                                     _ptr(out["s_row"]), _ptr(out["q_col"]), _ptr(out["s_col"]), _ptr(dev_err),
-                                     _stream(dev))
-    _check(st, "mx_token_logprobs_bwd")
+    row = _codes(out, "q_row", "s_row", T, Vp, layout, dev)
+    col = _codes(out, "q_col", "s_col", Vp, padded_rows(T, layout), layout, dev)
+    _launch("mx_token_logprobs_bwd", given, (x, targets, stats, entropy, dlogp, dent, _flag(dev_err)),
+            (x.data_ptr(), mx._DT[x.dtype], ld, T, V, targets.data_ptr(), ignore_index, stats.data_ptr(),
+             entropy.data_ptr(), _addr(dlogp), _addr(dent), scale, m, lay, *row, *col, _addr(dev_err)))
     return out
