@@ -26,6 +26,7 @@
 namespace mxk {
 
 constexpr float kLog2e = 1.44269504088896341f;
+constexpr double kLog2eD = 1.4426950408889634074;
 constexpr float kLn2 = 0.693147180559945309f;
 
 // 8 logits starting at element `i` of a row of n; `fill` past the end.
@@ -540,21 +541,82 @@ __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobArgs a, Split 
 
 // ---------------------------------------------------------------- backward
 
-// With l_j = (x_j - m) scale - ls, p_j = e^l_j and
-//   k1 = -scale dent, k0 = -scale (dlogp + dent entropy), add = scale dlogp
-// the gradient is p_j (k1 l_j + k0), plus `add` at the target. l is bounded
-// below where it multiplies k1, so that a masked entry gives p = 0 times a
-// finite number; a NaN still reaches the result through p.
+// With l_j = (x_j - m) scale - ls, p_j = e^l_j, the gradient is
+//   scale (dlogp ([j = target] - p_j) - dent p_j (l_j + entropy)).
+// In base 2, with c = scale log2(e) and K = m c + ls log2(e), p = 2^(x c - K).
+// The exponent is some 20 in size, where a float32 is spaced 2^-19: rounding it
+// would leave p off by 2^-20, ten times an ulp, and a probability's error
+// decides which way values next to a rounding border go (a block's scale can
+// hang on one). So K = ki + kf with ki an integer, n is the integer next to u =
+// x c - ki (its low bits appear where 1.5 * 2^23 is added), and f = x c -
+// (ki + n), about 1/2 in size, is one fused multiply-add: p = 2^f 2^n 2^-kf,
+// within an ulp or two. What c lost when it was rounded to float32, c (1 + r),
+// adds r (ki + n) to f; 2^-kf is folded into the row's constants.
+//
+// x is bounded below where u is -160 and p = 0: a masked entry then gives 0
+// times a finite number. (A NaN among the logits has made the row's statistics
+// NaN, and with them every constant.) Rows whose m c leaves no room for an
+// integer part (all entries at the lowest finite value) take their differences
+// from m first: base = m, else 0.
 struct GradRow {
-  float m, nls, k1, k0, add;
-  int32_t target;   // column within the tile, out of [0, 128) if elsewhere
+  float low;         // bound of x - base
+  float ki, mk;      // ki, 1.5 * 2^23 - ki
+  float k1, k0;      // gradient = 2^f 2^n (k1 u + k0)
+  float add;         // scale dlogp, at the target
+  float base;
+  int32_t target;    // column within the tile, out of [0, 128) if elsewhere
 };
+
+struct GradScale {
+  float c, r;
+};
+
+constexpr float kMagic = 12582912.0f;      // 1.5 * 2^23
+constexpr int32_t kMagicBits = 0x4B400000;
+
+template <bool FAR>
+__device__ __forceinline__ float grad_value(float x, const GradRow& g, GradScale c, float add) {
+  const float y = fmaxf(FAR ? x - g.base : x, g.low);
+  const float u = fmaf(y, c.c, -g.ki);
+  const float w = u + kMagic;
+  const float kn = w - g.mk;               // ki + n
+  const float f = fmaf(kn, c.r, fmaf(y, c.c, -kn));
+  const float p = ldexpf(__builtin_amdgcn_exp2f(f), __float_as_int(w) - kMagicBits);
+  return fmaf(p, fmaf(u, g.k1, g.k0), add);
+}
+
+template <bool F32, bool FAR>
+__device__ __forceinline__ uint4 grad_chunk(RawChunk<F32> raw, const GradRow& row, GradScale c, uint32_t col) {
+  // one chunk after the other: left to interleave four of them, the compiler
+  // takes 82 VGPRs, too many for a fourth tile on the CU (495 us against 460 at
+  // 4096 x 131072)
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i)
+    asm volatile("" : "+v"(raw.w[i].x), "+v"(raw.w[i].y), "+v"(raw.w[i].z), "+v"(raw.w[i].w) : : "memory");
+  const GradRow g = row;
+  float f[8];
+  if constexpr (F32) __builtin_memcpy(f, &raw, 32);
+  else unpack8(raw.w[0], f);
+  const uint32_t hit = (uint32_t)g.target - col;
+  if (hit < 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = grad_value<FAR>(f[k], g, c, (int)hit == k ? g.add : 0.0f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = grad_value<FAR>(f[k], g, c, 0.0f);
+  }
+  uint4 v = pack8(f);
+  asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
+  return v;
+}
 
 template <class F, bool F32, bool FULL>
 __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& l, GradRow* rows, int64_t r0, int64_t c0,
                                                  int rows_valid, int rows_pad, int cols_valid, int cols_pad) {
   constexpr int kB = F32 ? 4 : 2;
   const uint32_t t = threadIdx.x, cc = t & 15, tr = t >> 4;
+  const double cd0 = (double)a.scale * kLog2eD;
+  const GradScale c{(float)cd0, (float)((cd0 - (double)(float)cd0) / cd0)};
   const char* base = static_cast<const char*>(a.x) + (r0 * a.ld + c0) * kB;
   RawChunk<F32> raw[kChunks];
 #pragma unroll
@@ -573,44 +635,51 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
       else raw[j].w[0] = pack8(f);
     }
   }
+  bool row_far = false;
   if ((int)t < kTR) {
-    GradRow g{0.0f, 0.0f, 0.0f, 0.0f, 0.0f, -1};
+    GradRow g{};
+    g.mk = kMagic;
+    g.target = -1;
     if (FULL || (int)t < rows_valid) {
       const int64_t row = r0 + t;
       const float m = a.stats[2 * row], ls = a.stats[2 * row + 1];
       const int64_t tg = row_target(a, row);
       if (c0 == 0 && a.dev_err && tg < 0 && a.targets[row] != a.ignore_index) atomicOr(a.dev_err, 8);
       if (!(m == -INFINITY && ls == -INFINITY)) {   // a row with nothing left has gradient 0
+        const double cd = (double)a.scale * kLog2eD;
+        row_far = !(fabsf(m) * (float)cd <= 1048576.0f);
         const float d = tg >= 0 && a.dlogp ? a.dlogp[row] : 0.0f;
         const float dent = a.dent ? a.dent[row] : 0.0f;
-        g = GradRow{m, -ls, -a.scale * dent, -a.scale * (a.dent ? fmaf(dent, a.ent_in[row], d) : d), a.scale * d,
-                    tg >= c0 && tg < c0 + kTC ? (int32_t)(tg - c0) : -1};
+        const double K = fma(row_far ? 0.0 : (double)m, cd, (double)ls * kLog2eD);
+        const double ki = rint(K);
+        const float kf = (float)(K - ki);
+        const float fold = __builtin_amdgcn_exp2f(-kf);
+        const float k1 = -a.scale * kLn2 * dent;
+        const float k0 = fmaf(-k1, kf, -a.scale * (a.dent ? fmaf(dent, a.ent_in[row], d) : d));
+        g.ki = (float)ki;
+        g.low = (g.ki - 160.0f) / c.c;
+        g.mk = kMagic - g.ki;
+        g.k1 = k1 * fold;
+        g.k0 = k0 * fold;
+        g.base = row_far ? m : 0.0f;
+        g.add = a.scale * d;
+        g.target = tg >= c0 && tg < c0 + kTC ? (int32_t)(tg - c0) : -1;
       }
     }
     rows[t] = g;
   }
-  __syncthreads();
+  const bool far = __syncthreads_or(row_far);
   uint4 v[kChunks];
+  if (!far) {
 #pragma unroll
-  for (int j = 0; j < kChunks; ++j) {
-    const GradRow g = rows[tr + kRowStep * j];
-    float f[8];
-    if constexpr (F32) __builtin_memcpy(f, &raw[j], 32);
-    else unpack8(raw[j].w[0], f);
+    for (int j = 0; j < kChunks; ++j) v[j] = grad_chunk<F32, false>(raw[j], rows[tr + kRowStep * j], c, cc * 8);
+  } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float lp = fmaf(f[k] - g.m, a.scale, g.nls);
-      const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
-      f[k] = fmaf(p, fmaf(fmaxf(lp, -1e4f), g.k1, g.k0), 0.0f);
-    }
-    const uint32_t hit = (uint32_t)g.target - cc * 8;
-    if (hit < 8) {
+    for (int j = 0; j < kChunks; ++j) v[j] = grad_chunk<F32, true>(raw[j], rows[tr + kRowStep * j], c, cc * 8);
+  }
+  if constexpr (!FULL) {   // rows and columns that only fill up: +0
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if ((int)hit == k) f[k] += g.add;
-    }
-    v[j] = pack8(f);
-    if constexpr (!FULL) {   // rows and columns that only fill up: +0
+    for (int j = 0; j < kChunks; ++j) {
       const int left = (int)(tr + kRowStep * j) < rows_valid ? cols_valid - (int)cc * 8 : 0;
       uint32_t* w = reinterpret_cast<uint32_t*>(&v[j]);
 #pragma unroll
@@ -622,7 +691,7 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
 }
 
 template <class F, bool F32>
-__global__ __launch_bounds__(kFmtThreads) void k_logprob_bwd(LogprobArgs a) {
+__global__ __launch_bounds__(kFmtThreads, F32 ? 6 : 8) void k_logprob_bwd(LogprobArgs a) {
   __shared__ TileLds l;
   __shared__ GradRow rows[kTR];
   const TilePos at = tile_pos(blockIdx.x, (uint32_t)((a.vocab_pad + kTC - 1) / kTC), (uint32_t)((a.rows_pad + kTR - 1) / kTR),

@@ -215,3 +215,43 @@ def test_bwd_tile_orders_agree(gpu):
         assert torch.equal(out["q_row"][r], part["q_row"]) and torch.equal(out["s_row"][:, r], part["s_row"])
         assert torch.equal(out["q_col"][:, r0:r0 + n], part["q_col"])
         assert torch.equal(out["s_col"][r0 // 128:(r0 + n) // 128], part["s_col"])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [1.0, 1e-3, 40.0])
+def test_bwd_masks_and_magnitudes(gpu, dtype, scale):
+    """Rows masked by the lowest finite value, all at it (uniform), with a large
+    common offset, with one token far above the rest, and all masked, next to
+    ordinary rows in the same tile."""
+    V = 1001
+    low = torch.finfo(dtype).min
+    g = torch.Generator().manual_seed(4)
+    base = torch.randn(V, generator=g)
+    i = torch.arange(V)
+    spike = base.clone()
+    spike[17] = 300.0
+    rows = [base, torch.where(i % 3 == 0, base, torch.tensor(low)), torch.full((V,), low), base + 1000.0, base - 5000.0,
+            spike, torch.full((V,), -torch.inf), torch.where(i % 2 == 0, base, torch.tensor(-torch.inf)), base * 1e-20]
+    x = torch.stack(rows).to(dtype)
+    T = len(rows)
+    t = torch.full((T,), 18)
+    f = lm.token_logprobs(x.to(dev()), t.to(dev()), scale=scale)
+    dl, de = torch.linspace(-1, 1, T) + 0.05, torch.linspace(0.5, -0.5, T) + 0.01
+    out = lm.token_logprobs_bwd(x.to(dev()), t.to(dev()), f["stats"], f["entropy"], dl.to(dev()), de.to(dev()), scale=scale,
+                                layout="plain")
+    x64 = x.to(F64)
+    m, ls = f["stats"].cpu().to(F64).unbind(1)
+    ent = f["entropy"].cpu().to(F64)
+    grad = R.logprob_bwd(x64, t, m, ls, ent, dl.to(F64), de.to(F64), scale)
+    empty = (m == -torch.inf)[:, None]
+    lp = torch.where(empty | (x64 == -torch.inf), 0.0, (x64 - m[:, None]) * scale - ls[:, None])
+    p = torch.where(empty | (x64 == -torch.inf), 0.0, torch.exp(lp))
+    # an entry's own size bounds what its float32 difference from m can lose
+    size = torch.where(p > 0, 1 + scale * (x64.clamp(min=-1e30).abs() + torch.where(empty[:, 0], 0.0, m).abs()[:, None]) / 64,
+                       1.0)
+    size[2] = 1.0    # its differences are exact zeros
+    mag = scale * p * size * (dl.abs()[:, None] + de.abs()[:, None] * (1 + lp.abs() + ent.abs()[:, None]))
+    mag[:, 18] += scale * dl.abs()
+    Vp = lm.padded_rows(V, "plain")
+    pad = lambda v: torch.cat([v, v.new_zeros(T, Vp - V)], 1)
+    R.check_dual(out, pad(grad), "rceil", "plain", "grad", mag=pad(mag))
