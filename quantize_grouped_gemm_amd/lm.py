@@ -7,7 +7,10 @@ MXFP8 transformer runs between its GEMMs.
 
 Like the functions of mx: arguments are checked against the sizes that go with
 them, outputs are allocated with torch unless given in `out`, the library is
-called on torch's current stream, and there is no fallback. Codes and scales
+called on torch's current stream, and there is no fallback. Calls without
+given outputs go through _lmhost (C++), which takes about 6 us of host time
+where the steps below take 15 to 25; what it does not take as it is (given
+outputs, arguments to refuse) comes back and is checked here. Codes and scales
 are uint8 tensors under the keys q_row / s_row, q_col / s_col, q_ck / s_ck in
 the layouts of mx.quantize. The number of rows T is free; column-wise codes
 cover padded_rows(T, layout) rows, the ones past T being zeros, so they feed
@@ -25,6 +28,8 @@ IGNORE_INDEX = -100
 MAX_COLS = 16384      # longest row of the norm
 MAX_TOP = 64
 
+_NONE = (None, None)
+
 _P, _I64, _I32, _INT, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_float
 _SIGS = {
     "mx_add_rmsnorm_quant": ([_P, _I64, _P, _I64, _P, _I64, _I64, _F, _INT, _INT] + [_P] * 9, _INT),
@@ -39,6 +44,28 @@ _SIGS = {
 EXPORTS = tuple(_SIGS)
 
 _lib = None
+_host = None
+
+
+def host():
+    """The C++ host path (loaded once, with the library it calls)."""
+    global _host
+    if _host is None:
+        lib()
+        try:
+            from . import _lmhost
+        except ImportError as e:
+            raise MXError(f"_lmhost.so: {e}; build it with python -m quantize_grouped_gemm_amd.build") from None
+        _host = _lmhost
+    return _host
+
+
+def _done(res, name):
+    """The outputs of a call through _lmhost, or None if it was left to the
+    checks here; raises if the library refused it."""
+    if res.__class__ is int:
+        _check(res, name)
+    return res
 
 
 def lib():
@@ -127,9 +154,6 @@ def _codes(out, q, s, R, C, layout, dev):
     return out[q].data_ptr(), out[s].data_ptr()
 
 
-_NONE = (None, None)
-
-
 def _launch(name, given, tensors, args):
     """Checks that every tensor is on the current device and calls the library
     on torch's current stream. `given`: outputs that the caller passed."""
@@ -168,6 +192,11 @@ def add_rmsnorm_quant(x, w, r=None, eps=1e-6, mode="rceil", layout="k128", colwi
     with sum (with r; bf16), rstd (float32 [T]), q_row / s_row, with colwise
     q_col / s_col [C, padded_rows(T)], and with checkpoint q_ck / s_ck, the
     row-wise MXFP8 copy of s that add_rmsnorm_bwd takes in its place."""
+    if out is None:
+        res = _done((_host or host()).add_rmsnorm_quant(x, w, r, eps, mode, layout, colwise, checkpoint),
+                    "mx_add_rmsnorm_quant")
+        if res is not None:
+            return res
     m, lay = _format(mode, layout)
     T, C = shape = _matrix(x, "x")
     ld = _rows(x, "x", _BF, shape)
@@ -195,6 +224,12 @@ def add_rmsnorm_bwd(dy, w, rstd, x=None, checkpoint=None, dsum=None, mode="rceil
     and of r), dw (float32 [C]) and MXFP8 copies of dx: q_row / s_row and, with
     colwise, q_col / s_col. work: optional float32 scratch of bwd_work(T, C)
     elements."""
+    if out is None and work is None:
+        q_ck, s_ck = _NONE if checkpoint is None else checkpoint
+        res = _done((_host or host()).add_rmsnorm_bwd(dy, w, rstd, x, q_ck, s_ck, dsum, mode, layout, rowwise, colwise),
+                    "mx_add_rmsnorm_bwd")
+        if res is not None:
+            return res
     m, lay = _format(mode, layout)
     T, C = shape = _matrix(dy, "dy")
     ld = _rows(dy, "dy", _BF, shape)
@@ -239,6 +274,10 @@ def swiglu_ckpt_fwd(a, b, mode="rceil", layout="k128", out=None):
     of the w13 output). Returns q_row / s_row and q_col / s_col of h, and
     q_ck / s_ck, the row-wise MXFP8 copy of [a | b] [T, 2H] that
     swiglu_ckpt_bwd takes: the bf16 input need not be kept."""
+    if out is None:
+        res = _done((_host or host()).swiglu_ckpt_fwd(a, b, mode, layout), "mx_swiglu_ckpt_fwd")
+        if res is not None:
+            return res
     m, lay = _format(mode, layout)
     T, H = shape = _matrix(a, "a")
     ld = _rows(a, "a", _BF, shape)
@@ -256,6 +295,10 @@ def swiglu_ckpt_fwd(a, b, mode="rceil", layout="k128", out=None):
 def swiglu_ckpt_bwd(dh, q_ck, s_ck, mode="rceil", layout="k128", out=None):
     """Gradient of swiglu_ckpt_fwd from its checkpoint: dh bf16 [T, H] gives
     [dA | dB] [T, 2H] as q_row / s_row and q_col / s_col."""
+    if out is None:
+        res = _done((_host or host()).swiglu_ckpt_bwd(dh, q_ck, s_ck, mode, layout), "mx_swiglu_ckpt_bwd")
+        if res is not None:
+            return res
     m, lay = _format(mode, layout)
     T, H = shape = _matrix(dh, "dh")
     ld = _rows(dh, "dh", _BF, shape)
@@ -292,6 +335,10 @@ def token_logprobs(x, targets, scale=1.0, top=0, ignore_index=IGNORE_INDEX, out=
     descending order, ties to the lower index. Entries of -infinity are ruled
     out. dev_err: optional int32 device flag word; bit 3 reports a target
     outside the vocabulary (treated as not scored)."""
+    if out is None and dev_err is None:
+        res = _done((_host or host()).token_logprobs(x, targets, scale, top, ignore_index), "mx_token_logprobs")
+        if res is not None:
+            return res
     T, V, ld = _logits(x, targets, scale)
     if not 0 <= top <= min(MAX_TOP, V):
         raise MXError(f"top: {top}, expected 0 to {min(MAX_TOP, V)}")
@@ -316,6 +363,11 @@ def token_logprobs_bwd(x, targets, stats, entropy, dlogp=None, dent=None, scale=
     gradients of logp and entropy (None: zero). Returns q_row / s_row
     [T, V_pad] and q_col / s_col [V_pad, padded_rows(T)], with V_pad = V
     rounded up to the layout's block step (128 or 32) and zeros past V."""
+    if out is None and dev_err is None:
+        res = _done((_host or host()).token_logprobs_bwd(x, targets, stats, entropy, dlogp, dent, scale, mode, layout,
+                                                         ignore_index), "mx_token_logprobs_bwd")
+        if res is not None:
+            return res
     m, lay = _format(mode, layout)
     T, V, ld = _logits(x, targets, scale)
     _whole(stats, "stats", _F32, (T, 2))
