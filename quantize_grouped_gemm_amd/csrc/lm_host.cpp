@@ -98,11 +98,24 @@ struct Out {
   struct Codes {
     uint8_t *q = nullptr, *s = nullptr;
   };
+  // Codes and scales always go together, so they share one allocation: the
+  // scales 256-byte aligned behind the codes.
   Codes codes(PyObject* q, PyObject* s, int64_t R, int64_t C, const Format& f) {
-    Codes c;
-    c.q = static_cast<uint8_t*>(add(q, {R, C}, kU8));
-    c.s = static_cast<uint8_t*>(f.layout == MX_SCALES_K128 ? add(s, {C / 128, R, 4}, kU8) : add(s, {R, C / 32}, kU8));
-    return c;
+    const int64_t at = up(R * C, 256);
+    const Tensor base(at::detail::empty_cuda({at + R * C / 32}, kU8, device, std::nullopt));
+    uint8_t* p = static_cast<uint8_t*>(base.data_ptr());
+    part(q, base, 0, {R, C});
+    if (f.layout == MX_SCALES_K128) part(s, base, at, {C / 128, R, 4});
+    else part(s, base, at, {R, C / 32});
+    return Codes{p, p + at};
+  }
+  void part(PyObject* key, const Tensor& base, int64_t offset, at::IntArrayRef shape) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(), base.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(offset);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    PyObject* o = THPVariable_Wrap(std::move(t));
+    PyDict_SetItem(d, key, o);
+    Py_DECREF(o);
   }
   PyObject* done(mx_status st) {
     if (st != MX_OK) return PyLong_FromLong(st);

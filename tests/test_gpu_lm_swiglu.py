@@ -109,3 +109,25 @@ def test_special_values(gpu):
     R.check_codes(got["q_row"][:255, 32:], got["s_row"][:255, 1:], v[:, None].repeat(1, 32).clamp(max=2.0 ** 127),
                   "rceil", "dB")
     assert got["s_row"][255, 1] == 255
+
+
+def test_every_code_under_every_scale(gpu):
+    """The checkpoint's values for all 256 codes under all scale bytes: the
+    gradient from it equals the one from the dequantized bf16 tensor (exact for
+    scales whose values bf16 holds: E from -117 to 119). A NaN that arithmetic
+    produced has no defined sign: that bit is left out where the value is NaN."""
+    E = torch.arange(10, 247)
+    q = torch.arange(256, dtype=torch.uint8).repeat(E.numel(), 2).to(dev())          # a: all codes, b: all codes
+    s = E.to(torch.uint8)[:, None].repeat(1, 16).to(dev())
+    dh = torch.full((E.numel(), 256), 2.0 ** -60, dtype=BF, device=dev())
+    got = lm.swiglu_ckpt_bwd(dh, q, s, layout="plain")
+    z = mx.dequantize(q, s, BF)
+    T = lm.padded_rows(E.numel(), "plain")
+    zp = torch.zeros((T, 512), dtype=BF, device=dev())
+    zp[:E.numel()] = z
+    dp = torch.zeros((T, 256), dtype=BF, device=dev())
+    dp[:E.numel()] = dh
+    ref = mx.swiglu_quant_bwd(dp, zp[:, :256], zp[:, 256:], layout="plain")
+    assert torch.equal(got["s_row"], ref["s_row"][:E.numel()])
+    sign = torch.isnan(z[:, :256] + z[:, 256:]).to(torch.uint8).repeat(1, 2) * 0x80
+    assert torch.equal(got["q_row"] | sign, ref["q_row"][:E.numel()] | sign)
