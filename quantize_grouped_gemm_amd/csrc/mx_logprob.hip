@@ -111,10 +111,10 @@ struct RawChunk {
 // ---------------------------------------------------------------- forward
 //
 // One read of the logits. A workgroup streams its segment in tiles of
-// 256 x U chunks of 8; while it sums, each thread keeps the maximum of every
+// NT x U chunks of 8; while it sums, each thread keeps the maximum of every
 // *slot* of its share (a slot: the thread's chunks of one or a few tiles) in
 // LDS, at the cost of the maximum that the softmax needs anyway. The `top`
-// best entries then follow from the slots: the top-th largest of the 256
+// best entries then follow from the slots: the top-th largest of the
 // threads' maxima is a lower bound of the top-th largest entry, so only slots
 // that reach it can hold one (about `top` of some 4096), and only those are
 // read again, from cache.
@@ -124,9 +124,8 @@ struct RawChunk {
 // passes it by 2^32. One fused multiply-add forms the exponent, changes of r
 // are exact powers of two, and no per-element maximum is needed.
 
-constexpr int kThreads = 256;
 constexpr int kSlots = 16;
-constexpr int kRound = 4 * kThreads;        // entries looked at between two checks of the candidate count
+constexpr int kRound = 1024;                // entries looked at between two checks of the candidate count
 constexpr int kCand = kRound + kMaxTop;
 constexpr int kList = 512;                  // slots worth reading one by one
 constexpr float kNoRef = -1e30f;
@@ -156,12 +155,14 @@ __device__ __forceinline__ int count_larger(const uint64_t* keys, int n, uint64_
   return r;
 }
 
+template <int NT>
 struct TopLds {
-  uint16_t slot[kSlots][kThreads];
+  uint16_t slot[kSlots][NT];
   uint64_t cand[kCand];
   uint64_t best[kMaxTop];
   uint64_t thr;          // entries with a larger key are candidates
   uint16_t list[kList];
+  uint16_t tkey[NT];
   int count, hits;
 };
 
@@ -169,12 +170,13 @@ struct TopLds {
 // raises the threshold to the last of them once there are `top`. Keys are
 // unique, so an entry's rank is the number of larger ones. All threads call
 // it; barriers inside, the last one after the writes.
-__device__ __forceinline__ void keep_top(TopLds& l, int top) {
+template <int NT>
+__device__ __forceinline__ void keep_top(TopLds<NT>& l, int top) {
   const int t = threadIdx.x;
   __syncthreads();
   const int n = l.count;
 #pragma unroll 1
-  for (int i = t; i < n; i += kThreads) {
+  for (int i = t; i < n; i += NT) {
     const uint64_t key = l.cand[i];
     const int r = count_larger(l.cand, n, key);
     if (r < top) l.best[r] = key;
@@ -189,23 +191,28 @@ __device__ __forceinline__ void keep_top(TopLds& l, int top) {
   __syncthreads();
 }
 
-// Offers up to 4 entries per thread; all threads call it.
-template <bool F32>
-__device__ __forceinline__ void offer(TopLds& l, const void* x, int64_t i, int64_t n, bool on, uint32_t idx0, int top) {
+// Offers up to kRound / NT entries of a thread: those above the threshold
+// become candidates.
+template <bool F32, int NT>
+__device__ __forceinline__ void offer(TopLds<NT>& l, const void* x, int64_t i, int64_t n, uint32_t idx0) {
   const uint64_t thr = l.thr;
-  if (on) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (i + k < n) {
-        const float f = F32 ? static_cast<const float*>(x)[i + k]
-                            : __uint_as_float((uint32_t)static_cast<const uint16_t*>(x)[i + k] << 16);
-        const uint64_t key = top_key(f, idx0 + (uint32_t)(i + k));
-        if (key > thr) l.cand[atomicAdd(&l.count, 1)] = key;
-      }
+  for (int k = 0; k < kRound / NT; ++k) {
+    if (i + k < n) {
+      const float f = F32 ? static_cast<const float*>(x)[i + k]
+                          : __uint_as_float((uint32_t)static_cast<const uint16_t*>(x)[i + k] << 16);
+      const uint64_t key = top_key(f, idx0 + (uint32_t)(i + k));
+      if (key > thr) l.cand[atomicAdd(&l.count, 1)] = key;
     }
   }
+}
+
+// Between two rounds of offers: makes room if the next one might not fit. All
+// threads call it.
+template <int NT>
+__device__ __forceinline__ void make_room(TopLds<NT>& l, int top) {
   __syncthreads();
-  const bool full = l.count > kCand - kRound;   // the next round might not fit
+  const bool full = l.count > kCand - kRound;
   if (full) keep_top(l, top);
   else __syncthreads();
 }
@@ -213,26 +220,25 @@ __device__ __forceinline__ void offer(TopLds& l, const void* x, int64_t i, int64
 // The `top` best entries of the segment [0, n) of x (first index idx0), in
 // descending order in l.cand[0 .. l.count). `slots` slots of `tiles` tiles
 // each; tmax the thread's maximum.
-template <bool F32>
-__device__ __forceinline__ void find_top(TopLds& l, const void* x, int64_t n, uint32_t idx0, float tmax, int slots,
+template <bool F32, int NT>
+__device__ __forceinline__ void find_top(TopLds<NT>& l, const void* x, int64_t n, uint32_t idx0, float tmax, int slots,
                                          int tiles, int top) {
   constexpr int U = kUnroll<F32>;
   const int t = threadIdx.x;
-  __shared__ uint16_t tkey[kThreads];
-  tkey[t] = (uint16_t)key16(tmax);
+  l.tkey[t] = (uint16_t)key16(tmax);
   if (t == 0) l.count = l.hits = 0;
   __syncthreads();
   if (t < 64) {
-    // the top-th largest of the 256 keys, bit by bit
-    uint32_t k[4];
+    // the top-th largest of the NT keys, bit by bit
+    uint32_t k[NT / 64];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) k[i] = tkey[t + 64 * i];
+    for (int i = 0; i < NT / 64; ++i) k[i] = l.tkey[t + 64 * i];
     uint32_t bound = 0;
     for (int b = 15; b >= 0; --b) {
       const uint32_t tryb = bound | (1u << b);
       int c = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c += __popcll(__ballot(k[i] >= tryb));
+      for (int i = 0; i < NT / 64; ++i) c += __popcll(__ballot(k[i] >= tryb));
       if (c >= top) bound = tryb;
     }
     if (t == 0) l.thr = bound ? ((uint64_t)bound << 48) - 1 : 0;
@@ -242,33 +248,40 @@ __device__ __forceinline__ void find_top(TopLds& l, const void* x, int64_t n, ui
   for (int s = 0; s < slots; ++s) {
     if (l.slot[s][t] >= bound) {
       const int at = atomicAdd(&l.hits, 1);
-      if (at < kList) l.list[at] = (uint16_t)(s * kThreads + t);
+      if (at < kList) l.list[at] = (uint16_t)(s * NT + t);
     }
   }
   __syncthreads();
   const int hits = l.hits;
-  const int per = 2 * U * tiles;    // half chunks of a slot
+  constexpr int kEach = kRound / NT;           // entries per thread and round
+  const int per = 8 / kEach * U * tiles;       // such pieces of a slot
+  const int64_t items = (int64_t)hits * per;
   if (hits <= kList) {
-    for (int base = 0; base < hits * per; base += kThreads) {
-      const int item = base + t;
-      const bool on = item < hits * per;
-      const int e = on ? l.list[item / per] : 0, h = item % per;
-      const int64_t chunk = ((int64_t)(e / kThreads) * tiles * U + (h >> 1)) * kThreads + e % kThreads;
-      offer<F32>(l, x, 8 * chunk + 4 * (h & 1), n, on, idx0, top);
+    for (int64_t base = 0; base < items; base += NT) {
+      const int item = (int)base + t;
+      if (item < items) {
+        const int e = l.list[item / per], h = item % per;
+        const int64_t chunk = ((int64_t)(e / NT) * tiles * U + h / (8 / kEach)) * NT + e % NT;
+        offer<F32, NT>(l, x, 8 * chunk + kEach * (h % (8 / kEach)), n, idx0);
+      }
+      if (items * kEach > kCand) make_room(l, top);
     }
   } else {
     // so many slots qualify (equal or sorted entries): read the segment again
-    for (int64_t base = 0; base < n; base += kRound) offer<F32>(l, x, base + 4 * t, n, true, idx0, top);
+    for (int64_t base = 0; base < n; base += kRound) {
+      offer<F32, NT>(l, x, base + kEach * t, n, idx0);
+      make_room(l, top);
+    }
   }
   keep_top(l, top);
 }
 
 // S and A of the segment relative to its maximum m, by the definition; for
 // maxima whose exponents the fast sums cannot hold.
-template <bool F32>
+template <bool F32, int NT>
 __device__ __forceinline__ Soft far_sums(const void* x, int64_t n, float m, float c) {
   Soft v{m, 0.0f, 0.0f};
-  for (int64_t i = 8 * (int64_t)threadIdx.x; i < n; i += 8 * kThreads) {
+  for (int64_t i = 8 * (int64_t)threadIdx.x; i < n; i += 8 * NT) {
     float f[8];
     load_logits<F32>(x, i, n, -INFINITY, f);
 #pragma unroll
@@ -320,13 +333,16 @@ __device__ __forceinline__ RowOut store_row(const LogprobArgs& a, int64_t row, S
   return RowOut{v.m, ls, empty};
 }
 
-// Joins the Softs of a wave's first 32 lanes (every wave does the same work)
+constexpr int kMaxParts = 16;
+constexpr int kJoinThreads = 256;
+
+// Joins the Softs of a wave's first kMaxParts lanes (every wave does the same work)
 // and stores the row.
 template <bool F32>
 __device__ __forceinline__ RowOut join_row(const LogprobArgs& a, int64_t row, Soft v, float c) {
   const TargetLogit tl = target_logit<F32>(a, row);
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1)
+  for (int o = kMaxParts / 2; o >= 1; o >>= 1)
     v = soft_join(v, Soft{__shfl_xor(v.m, o), __shfl_xor(v.s, o), __shfl_xor(v.a, o)}, c);
   v = Soft{__shfl(v.m, 0), __shfl(v.s, 0), __shfl(v.a, 0)};
   return store_row(a, row, v, tl);
@@ -363,12 +379,12 @@ __device__ __forceinline__ PartWork part_work(const LogprobArgs& a, const Split&
   return PartWork{reinterpret_cast<Soft*>(w), reinterpret_cast<uint64_t*>(w + soft_bytes(a.rows, sp.parts))};
 }
 
-template <bool F32, bool TOP>
-__global__ __launch_bounds__(kThreads) void k_logprob_part(LogprobArgs a, Split sp) {
+template <bool F32, bool TOP, int NT>
+__global__ __launch_bounds__(NT) void k_logprob_part(LogprobArgs a, Split sp) {
   constexpr int U = kUnroll<F32>;
-  constexpr int kTile = 8 * U * kThreads;
-  __shared__ float red[3][4];
-  __shared__ std::conditional_t<TOP, TopLds, int> l;
+  constexpr int kTile = 8 * U * NT, kWaves = NT / 64;
+  __shared__ float red[3][kWaves];
+  __shared__ std::conditional_t<TOP, TopLds<NT>, int> l;
   const int t = threadIdx.x;
   const int64_t row = blockIdx.x / (unsigned)sp.parts;
   const int64_t part = blockIdx.x - row * sp.parts;
@@ -386,12 +402,12 @@ __global__ __launch_bounds__(kThreads) void k_logprob_part(LogprobArgs a, Split 
     if (base + kTile <= n) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        __builtin_memcpy(&r[u], x + (base + 8 * kThreads * u) * (F32 ? 4 : 2) + 8 * t * (F32 ? 4 : 2), sizeof(r[u]));
+        __builtin_memcpy(&r[u], x + (base + 8 * NT * u) * (F32 ? 4 : 2) + 8 * t * (F32 ? 4 : 2), sizeof(r[u]));
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float f[8];
-        const int64_t i = base + 8 * (kThreads * u + t);
+        const int64_t i = base + 8 * (NT * u + t);
         if (i < n) load_logits<F32>(x, i, n, -INFINITY, f);
         else
 #pragma unroll
@@ -449,10 +465,12 @@ __global__ __launch_bounds__(kThreads) void k_logprob_part(LogprobArgs a, Split 
   for (int o = 32; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
   if ((t & 63) == 0) red[0][t >> 6] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  M = red[0][0];
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) M = fmaxf(M, red[0][i]);
   Soft v;
   if (M != -INFINITY && !(fabsf(M) * c <= kFarExp)) {
-    v = far_sums<F32>(x, n, M, c);
+    v = far_sums<F32, NT>(x, n, M, c);
   } else {
     // relative to M itself: r - M c, then the factor 2^(r - M c)
     const float base = M == -INFINITY ? 0.0f : M;
@@ -470,10 +488,15 @@ __global__ __launch_bounds__(kThreads) void k_logprob_part(LogprobArgs a, Split 
     red[2][t >> 6] = v.a;
   }
   __syncthreads();
-  v.s = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  v.a = (red[2][0] + red[2][1]) + (red[2][2] + red[2][3]);
+  v.s = red[1][0];
+  v.a = red[2][0];
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) {
+    v.s += red[1][i];
+    v.a += red[2][i];
+  }
 
-  if constexpr (TOP) find_top<F32>(l, x, n, (uint32_t)first, tmax, slot, per_slot, a.top);
+  if constexpr (TOP) find_top<F32, NT>(l, x, n, (uint32_t)first, tmax, slot, per_slot, a.top);
   if (sp.parts == 1) {
     const RowOut o = store_row(a, row, v, tl);
     if constexpr (TOP) store_top(a, row, l.cand, o);
@@ -486,14 +509,13 @@ __global__ __launch_bounds__(kThreads) void k_logprob_part(LogprobArgs a, Split 
   }
 }
 
-constexpr int kMaxParts = 32;
 
 // One workgroup per row. The alternatives: the top-th largest of the lists'
 // first entries (`lead` of each, at least `top` in all) bounds the result from
 // below; what reaches it, rarely many more than `top`, is ranked. All loads of
 // global memory are issued at the start: the kernel is a chain of latencies.
 template <bool F32, bool TOP>
-__global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobArgs a, Split sp) {
+__global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobArgs a, Split sp) {
   const int t = threadIdx.x, lane = t & 63;
   const int64_t row = blockIdx.x;
   const PartWork w = part_work(a, sp);
@@ -506,7 +528,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobArgs a, Split 
     __shared__ int count;
     const int total = sp.parts * a.top;
     const uint64_t* src = w.keys + row * total;
-    for (int i = t; i < total; i += kThreads) keys[i] = src[i];
+    for (int i = t; i < total; i += kJoinThreads) keys[i] = src[i];
     if (t == 0) {
       bound = 1;
       count = 0;
@@ -521,13 +543,13 @@ __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobArgs a, Split 
     if (t < leads && k0 && count_larger(cand, leads, k0) == a.top - 1) bound = k0;
     __syncthreads();
     const uint64_t b = bound;
-    for (int i = t; i < total; i += kThreads) {
+    for (int i = t; i < total; i += kJoinThreads) {
       const uint64_t k = keys[i];
       if (k >= b) cand[atomicAdd(&count, 1)] = k;
     }
     __syncthreads();
     const int n = count;
-    for (int i = t; i < n; i += kThreads) {
+    for (int i = t; i < n; i += kJoinThreads) {
       const uint64_t k = cand[i];
       const int r = count_larger(cand, n, k);
       if (r < a.top) best[r] = k;
@@ -709,14 +731,25 @@ __global__ __launch_bounds__(kFmtThreads, F32 ? 6 : 8) void k_logprob_bwd(Logpro
 
 // ---------------------------------------------------------------- launch
 
-// Few rows are split over the vocabulary so that about 1024 workgroups run
-// (4 per CU), into segments of at least 4096 logits.
+// A row is split over the vocabulary, into up to 16 segments of at least 8192
+// logits, where rows are few and long: the join costs a launch and 5 us. One
+// row of 131072 with 20 alternatives takes 11.2 us in 16 segments and 17.2
+// whole, 64 such rows 12.9 and 20.0; 200 rows take 21 either way, and rows of
+// up to 65536 are faster whole (84 x 48907 13.0 against 14.0, one row of 50000
+// 11.0 against 11.3).
 static Split split_rows(int64_t rows, int64_t vocab) {
   int64_t parts = 1;
-  while (parts < kMaxParts && rows * parts < 1024 && vocab / (2 * parts) >= 4096) parts *= 2;
+  if (rows <= 128 && vocab > 65536)
+    while (parts < kMaxParts && rows * parts < 1024 && vocab / (2 * parts) >= 8192) parts *= 2;
   const int64_t seg = ((vocab + parts - 1) / parts + 7) / 8 * 8;
   return Split{(int32_t)((vocab + seg - 1) / seg), seg};
 }
+
+// Threads of a workgroup: 512 where every CU gets at most one of them and its
+// segment is long (200 x 131072: 17.5 us against 21.4 with 256, 84 x 48907 12.2
+// against 13.0), else 256 (500 x 131072: 26.9 against 29.5 with 512, 128 x 8520
+// 6.9 against 7.4).
+static bool wide_groups(int64_t groups, int64_t seg) { return groups <= 256 && seg >= 32768; }
 
 int64_t logprob_work(int64_t rows, int64_t vocab, int32_t top) {
   const Split sp = split_rows(rows, vocab);
@@ -726,10 +759,14 @@ int64_t logprob_work(int64_t rows, int64_t vocab, int32_t top) {
 template <bool F32, bool TOP>
 static hipError_t launch_fwd(const LogprobArgs& a, hipStream_t s) {
   const Split sp = split_rows(a.rows, a.vocab);
-  hipLaunchKernelGGL((k_logprob_part<F32, TOP>), dim3((unsigned)(a.rows * sp.parts)), dim3(kThreads), 0, s, a, sp);
+  const dim3 grid((unsigned)(a.rows * sp.parts));
+  if (wide_groups(a.rows * sp.parts, sp.seg))
+    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 512>), grid, dim3(512), 0, s, a, sp);
+  else
+    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 256>), grid, dim3(256), 0, s, a, sp);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || sp.parts == 1) return e;
-  hipLaunchKernelGGL((k_logprob_join<F32, TOP>), dim3((unsigned)a.rows), dim3(kThreads), 0, s, a, sp);
+  hipLaunchKernelGGL((k_logprob_join<F32, TOP>), dim3((unsigned)a.rows), dim3(kJoinThreads), 0, s, a, sp);
   return hipGetLastError();
 }
 

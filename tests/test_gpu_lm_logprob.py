@@ -255,3 +255,12 @@ def test_bwd_masks_and_magnitudes(gpu, dtype, scale):
     Vp = lm.padded_rows(V, "plain")
     pad = lambda v: torch.cat([v, v.new_zeros(T, Vp - V)], 1)
     R.check_dual(out, pad(grad), "rceil", "plain", "grad", mag=pad(mag))
+
+
+@pytest.mark.parametrize("T,V,top,dtype", [(128, 70000, 9, BF), (129, 70000, 9, BF), (100, 65536, 5, F32), (9, 65537, 64, BF),
+                                           (2, 200003, 64, F32), (257, 32768, 3, BF), (256, 32768, 3, BF)])
+def test_fwd_around_the_launch_rules(gpu, T, V, top, dtype):
+    """Both sides of the limits where rows are split and workgroups widened."""
+    x, t = _logits(T, V, dtype, V - T)
+    print(f"T={T} V={V} top={top} {dtype}", flush=True)
+    _check_fwd(lm.token_logprobs(x, t, top=top), x, t, 1.0, top)
