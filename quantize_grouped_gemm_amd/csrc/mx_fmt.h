@@ -96,10 +96,11 @@ __device__ __forceinline__ uint32_t floor_limit2(uint32_t sb) {
   return lim | (lim << 16);
 }
 
-// cvt4 without a defined starting value (both halves are written).
+// cvt4 without a defined starting value (both halves are written; the empty
+// asm stands for a register of any content, a zero would cost a move).
 __device__ __forceinline__ uint32_t cvt4u(uint32_t w0, uint32_t w1, float scale) {
   mx_v2s r;
-  r = __builtin_nondeterministic_value(r);
+  asm volatile("" : "=v"(r));
   r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(mx_v2bf, w0), scale, false);
   r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(mx_v2bf, w1), scale, true);
   return __builtin_bit_cast(uint32_t, r);
@@ -173,10 +174,14 @@ __device__ __forceinline__ void fmt_rowq(const uint4 (&v)[kChunks], int rows_val
   }
 }
 
+// Chunk j of row r = tr + 32 j goes to slot lds_unit(r, cc): as tr >> 4 is 0 or
+// 1, the swizzle's 2 ((r >> 4) & 7) is 2 (tr >> 4) + 4 j, and the slot is chunk
+// 0's with 4 j XORed into its unit.
 __device__ __forceinline__ void fmt_to_lds(const uint4 (&v)[kChunks], TileLds& l) {
-  const int t = threadIdx.x;
+  const uint32_t t = threadIdx.x, tr = t >> 4;
+  const uint32_t slot = lds_unit(tr, t & 15);
 #pragma unroll
-  for (int j = 0; j < kChunks; ++j) l.v[lds_unit((t >> 4) + kRowStep * j, t & 15)] = v[j];
+  for (int j = 0; j < kChunks; ++j) l.v[(slot ^ (4 * j)) + 16 * kRowStep * j] = v[j];
 }
 
 // Column-wise codes from the LDS copy: lane l of wave w takes rows 16 q .. 16 q

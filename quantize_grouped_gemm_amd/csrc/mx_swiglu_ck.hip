@@ -116,7 +116,7 @@ __device__ __forceinline__ void swiglu_ck_bwd_tile(const SwigluCkArgs& a, TileLd
 }
 
 template <class F>
-__global__ __launch_bounds__(kFmtThreads, 8) void k_swiglu_ck_bwd(SwigluCkArgs a) {
+__global__ __launch_bounds__(kFmtThreads) void k_swiglu_ck_bwd(SwigluCkArgs a) {
   __shared__ TileLds l;
   const TilePos at = tile_pos(blockIdx.x, (uint32_t)((a.hidden + kTC - 1) / kTC), (uint32_t)((a.rows_pad + kTR - 1) / kTR),
                               a.bands);
