@@ -16,8 +16,9 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t)65535 * 128;   // one grid row per 128 tokens
 
-// The tile kernels address the 16 rows between two of a thread's chunks with
-// 32-bit byte offsets.
+// The tile kernels address the 32 rows between two of a thread's chunks with
+// 32-bit byte offsets: 31 strides of 2^27 bytes stay below 2^32, so 2^26
+// elements of bf16 and 2^25 of float32.
 constexpr int64_t kMaxStride = 1ll << 26;
 
 // One workgroup of 512 threads per 128 x 128 tile; a grid holds 2^32 threads.
@@ -242,7 +243,9 @@ mx_status mx_token_logprobs_bwd(const void* x, mx_dtype x_dtype, int64_t ld, int
   const char* fn = "mx_token_logprobs_bwd";
   MX_CHECK(check_format(fn, mode, layout));
   MX_CHECK(check_logits(fn, x, x_dtype, ld, rows, vocab, scale));
-  MX_REQUIRE(vocab <= kMaxStride - 128 && ld <= kMaxStride, MX_ERR_SHAPE, "%s: vocab or ld above 2^26", fn);
+  const int64_t max_ld = x_dtype == MX_F32 ? kMaxStride / 2 : kMaxStride;
+  MX_REQUIRE(vocab <= max_ld - 128 && ld <= max_ld, MX_ERR_SHAPE, "%s: vocab (%lld) or ld (%lld) above %lld", fn,
+             (long long)vocab, (long long)ld, (long long)max_ld);
   MX_REQUIRE(tiles_fit(rows, vocab), MX_ERR_SHAPE, "%s: too many tiles for one launch", fn);
   if (rows == 0) return MX_OK;
   MX_REQUIRE(targets && stats && entropy, MX_ERR_NULL, "%s: targets/stats/entropy NULL", fn);

@@ -212,3 +212,15 @@ def test_abi_refusals():
     assert lb(layout=2) == 4 and lb(mode=5) == 4 and lb(q=None) == 1 and lb(q=odd) == 3 and lb(stats=None) == 1
     if not torch.cuda.is_available():
         assert fwd() == 5 and bwd() == 5 and lp() == 5 and lb() == 5 and L.mx_last_error()
+
+
+@pytest.mark.parametrize("dt,limit", [(0, 1 << 26), (1, 1 << 25)])
+def test_logit_gradient_strides_are_bounded_in_bytes(dt, limit):
+    L, p = lm.lib(), ctypes.c_void_p(16)
+
+    def status(ld, vocab=1000):
+        return L.mx_token_logprobs_bwd(p, dt, ld, 4, vocab, p, -100, p, p, p, p, 1.0, 0, 1, p, p, p, p, None, None)
+
+    assert status(limit + 8) == 2 and status(limit, limit) == 2
+    if not torch.cuda.is_available():
+        assert status(limit) == 5 and status(limit, limit - 128) == 5
