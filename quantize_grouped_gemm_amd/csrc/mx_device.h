@@ -40,6 +40,25 @@ __device__ __forceinline__ uint4 load_stream16(const void* p) {
   return make_uint4(q.x, q.y, q.z, q.w);
 }
 
+// The same for 8 bytes, and for stores of lines that the kernels right behind
+// do not read (or that are too many for the 256 MB Infinity Cache to hold until
+// they do): such lines leave the cache to the others.
+__device__ __forceinline__ uint2 load_stream8(const void* p) {
+  typedef unsigned v2u __attribute__((ext_vector_type(2)));
+  const v2u q = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(p));
+  return make_uint2(q.x, q.y);
+}
+
+__device__ __forceinline__ void store_stream8(void* p, uint2 v) {
+  typedef unsigned v2u __attribute__((ext_vector_type(2)));
+  __builtin_nontemporal_store((v2u){v.x, v.y}, reinterpret_cast<v2u*>(p));
+}
+
+__device__ __forceinline__ void store_stream16(void* p, uint4 v) {
+  typedef unsigned v4u __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store((v4u){v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(p));
+}
+
 // max |v| over the 8 bf16 values of a 16-byte chunk, as 15-bit magnitude bits
 // (non-negative bf16 bit patterns order like their values; NaN > 0x7F80).
 __device__ __forceinline__ uint32_t absmax8_bits(uint4 v) {

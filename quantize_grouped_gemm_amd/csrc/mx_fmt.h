@@ -139,9 +139,22 @@ __device__ __forceinline__ void fmt_load(uint4 (&v)[kChunks], const uint16_t* ba
   }
 }
 
+// Codes of 8 (16) values, non-temporal with STREAM.
+template <bool STREAM>
+__device__ __forceinline__ void store_codes(uint8_t* p, uint2 v) {
+  if constexpr (STREAM) store_stream8(p, v);
+  else *reinterpret_cast<uint2*>(p) = v;
+}
+
+template <bool STREAM>
+__device__ __forceinline__ void store_codes(uint8_t* p, uint4 v) {
+  if constexpr (STREAM) store_stream16(p, v);
+  else *reinterpret_cast<uint4*>(p) = v;
+}
+
 // Row-wise codes of the tile from the threads' chunks; scale bytes to s_row.
 // All threads must reach this function.
-template <class F, bool FULL>
+template <class F, bool FULL, bool STREAM>
 __device__ __forceinline__ void fmt_rowq(const uint4 (&v)[kChunks], int rows_valid, int cols_valid,
                                          const TileOut& o, int64_t r0, int64_t c0, uint32_t* s_row) {
   const uint32_t t = threadIdx.x, cc = t & 15, tr = t >> 4;
@@ -165,7 +178,7 @@ __device__ __forceinline__ void fmt_rowq(const uint4 (&v)[kChunks], int rows_val
       codes = e4m3_chunk(v[j], sb[j], !F::rceil);
     }
     if (FULL || ((int)tr + kRowStep * j < rows_valid && (int)cc * 8 < cols_valid))
-      *reinterpret_cast<uint2*>(base + (int64_t)(kRowStep * j) * o.ld + off) = codes;
+      store_codes<STREAM>(base + (int64_t)(kRowStep * j) * o.ld + off, codes);
   }
   if ((t & 3) == 0) {
     uint8_t* s = reinterpret_cast<uint8_t*>(s_row) + tr * 4 + (cc >> 2);
@@ -189,7 +202,7 @@ __device__ __forceinline__ void fmt_to_lds(const uint4 (&v)[kChunks], TileLds& l
 // 8 lanes of a column pair cover 128 codes of two output rows; scale bytes to
 // s_col. rows_valid counts the rows that are written, zero rows
 // included.
-template <class F, bool FULL>
+template <class F, bool FULL, bool STREAM>
 __device__ __forceinline__ void fmt_colq(TileLds& l, int rows_valid, int cols_valid, const TileOut& o, int64_t r0,
                                          int64_t c0) {
   const uint32_t* lds = reinterpret_cast<const uint32_t*>(l.v);
@@ -241,8 +254,8 @@ __device__ __forceinline__ void fmt_colq(TileLds& l, int rows_valid, int cols_va
   }
   if (FULL || ((int)(2 * cp) < cols_valid && (int)(16 * q) < rows_valid)) {
     const uint32_t off = 2 * cp * (uint32_t)o.ld + 16 * q;
-    *reinterpret_cast<uint4*>(base + off) = make_uint4(c0w[0], c0w[1], c0w[2], c0w[3]);
-    *reinterpret_cast<uint4*>(base + o.ld + off) = make_uint4(c1w[0], c1w[1], c1w[2], c1w[3]);
+    store_codes<STREAM>(base + off, make_uint4(c0w[0], c0w[1], c0w[2], c0w[3]));
+    store_codes<STREAM>(base + o.ld + off, make_uint4(c1w[0], c1w[1], c1w[2], c1w[3]));
   }
   if ((lane & 1) == 0) {
     uint8_t* sp = reinterpret_cast<uint8_t*>(l.s_col) + 8 * cp + (q >> 1);
@@ -271,15 +284,15 @@ __device__ __forceinline__ void fmt_scales(const uint32_t* s, int i, int lines, 
 
 // Both directions of the tile in v (column-wise with rows_pad >= rows_valid
 // rows, the extra ones zeros). Holds barriers; ends with one if `more` work
-// on the same LDS follows.
-template <class F, bool FULL>
+// on the same LDS follows. RS, CS: row-wise, column-wise codes non-temporal.
+template <class F, bool FULL, bool RS, bool CS>
 __device__ __forceinline__ void fmt_dual(const uint4 (&v)[kChunks], TileLds& l, int rows_valid, int rows_pad,
                                          int cols_valid, const TileOut& orow, const TileOut& ocol, int64_t r0,
                                          int64_t crow, bool more) {
-  fmt_rowq<F, FULL>(v, rows_valid, cols_valid, orow, r0, crow, l.s_row);
+  fmt_rowq<F, FULL, RS>(v, rows_valid, cols_valid, orow, r0, crow, l.s_row);
   fmt_to_lds(v, l);
   __syncthreads();
-  fmt_colq<F, FULL>(l, rows_pad, cols_valid, ocol, r0, crow);
+  fmt_colq<F, FULL, CS>(l, rows_pad, cols_valid, ocol, r0, crow);
   __syncthreads();
   const int t = threadIdx.x;
   if (t < kTR) fmt_scales<F>(l.s_row, t, rows_valid, cols_valid, orow, r0, crow);
@@ -290,7 +303,7 @@ __device__ __forceinline__ void fmt_dual(const uint4 (&v)[kChunks], TileLds& l, 
 // Quantizes one chunk of row `row` at column `col` (a multiple of 8) and
 // stores its codes and its block's or step's scales. All lanes must reach
 // this function; `ok` (uniform over each quad) guards the stores.
-template <class F>
+template <class F, bool STREAM>
 __device__ __forceinline__ void fmt_chunk(uint4 v, bool ok, const TileOut& o, int64_t row, uint32_t col) {
   const uint32_t m = quad_max_hi(absmax8_hi(v));
   uint32_t sb;
@@ -307,11 +320,11 @@ __device__ __forceinline__ void fmt_chunk(uint4 v, bool ok, const TileOut& o, in
     packed |= dpp<0x124>(packed);
     packed |= dpp<0x128>(packed);
     if (ok) {
-      *reinterpret_cast<uint2*>(o.q + row * o.ld + col) = codes;
+      store_codes<STREAM>(o.q + row * o.ld + col, codes);
       if ((col & 127) == 0) *reinterpret_cast<uint32_t*>(o.s + ((int64_t)(col >> 7) * o.srows + row) * 4) = packed;
     }
   } else if (ok) {
-    *reinterpret_cast<uint2*>(o.q + row * o.ld + col) = codes;
+    store_codes<STREAM>(o.q + row * o.ld + col, codes);
     if ((col & 31) == 0) o.s[row * (o.ld / kBlock) + (col >> 5)] = (uint8_t)sb;
   }
 }

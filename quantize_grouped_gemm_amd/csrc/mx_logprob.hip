@@ -108,6 +108,20 @@ struct RawChunk {
   uint4 w[F32 ? 2 : 1];
 };
 
+// 8 logits at p, aligned to their element only.
+template <bool F32, bool STREAM>
+__device__ __forceinline__ RawChunk<F32> load_raw(const char* p) {
+  typedef unsigned v4u __attribute__((ext_vector_type(4), aligned(2)));
+  RawChunk<F32> r;
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+    const v4u* q = reinterpret_cast<const v4u*>(p + 16 * i);
+    const v4u v = STREAM ? __builtin_nontemporal_load(q) : *q;
+    r.w[i] = make_uint4(v.x, v.y, v.z, v.w);
+  }
+  return r;
+}
+
 // ---------------------------------------------------------------- forward
 //
 // One read of the logits. A workgroup streams its segment in tiles of
@@ -379,7 +393,7 @@ __device__ __forceinline__ PartWork part_work(const LogprobArgs& a, const Split&
   return PartWork{reinterpret_cast<Soft*>(w), reinterpret_cast<uint64_t*>(w + soft_bytes(a.rows, sp.parts))};
 }
 
-template <bool F32, bool TOP, int NT>
+template <bool F32, bool TOP, int NT, bool STREAM>
 __global__ __launch_bounds__(NT) void k_logprob_part(LogprobArgs a, Split sp) {
   constexpr int U = kUnroll<F32>;
   constexpr int kTile = 8 * U * NT, kWaves = NT / 64;
@@ -402,7 +416,7 @@ __global__ __launch_bounds__(NT) void k_logprob_part(LogprobArgs a, Split sp) {
     if (base + kTile <= n) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        __builtin_memcpy(&r[u], x + (base + 8 * NT * u) * (F32 ? 4 : 2) + 8 * t * (F32 ? 4 : 2), sizeof(r[u]));
+        r[u] = load_raw<F32, STREAM>(x + (base + 8 * NT * u) * (F32 ? 4 : 2) + 8 * t * (F32 ? 4 : 2));
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -569,46 +583,50 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobArgs a, Sp
 // The exponent is some 20 in size, where a float32 is spaced 2^-19: rounding it
 // would leave p off by 2^-20, ten times an ulp, and a probability's error
 // decides which way values next to a rounding border go (a block's scale can
-// hang on one). So K = ki + kf with ki an integer, n is the integer next to u =
-// x c - ki (its low bits appear where 1.5 * 2^23 is added), and f = x c -
-// (ki + n), about 1/2 in size, is one fused multiply-add: p = 2^f 2^n 2^-kf,
-// within an ulp or two. What c lost when it was rounded to float32, c (1 + r),
-// adds r (ki + n) to f; 2^-kf is folded into the row's constants.
+// hang on one). So K = ki + kf with ki an integer, and with the integer n next
+// to x c - ki (it appears in the low bits of w = x c - ki + 1.5 * 2^23, one
+// fused multiply-add), f = x c - (ki + n), about 1/2 in size, is another one:
+// p = 2^f 2^n 2^-kf, where 2^n is added to the exponent field and 2^-kf is
+// folded into the row's constants. What c lost when it was rounded to float32,
+// c (1 + r), would add r x c to the exponent; K takes its value at p = 2^-16, and
+// what is left, r (16 + log2 p), is 2^-20 at most (2^-22 for scale 1), at p near 1.
 //
-// x is bounded below where u is -160 and p = 0: a masked entry then gives 0
-// times a finite number. (A NaN among the logits has made the row's statistics
-// NaN, and with them every constant.) Rows whose m c leaves no room for an
-// integer part (all entries at the lowest finite value) take their differences
-// from m first: base = m, else 0.
+// The kernel is as close to its VALU issue rate as to HBM's: these 11 slots a
+// logit (4 of them v_exp_f32) in place of 14, with c's correction and the scaling
+// by 2^n as instructions of their own, take 4096 x 131072 from 429 to 407 us
+// (5.4 TB/s) and 6000 x 100001 from 588 to 565.
+//
+// x is bounded below where x c - ki is -186: a masked entry then gives 2^-186
+// times a finite number, 0 in bf16 for every gradient below 2^52. The exponent
+// field holds n + 64, which keeps it positive, and the constants the factor
+// 2^-64. (A NaN among the logits has made the row's statistics NaN, and with
+// them every constant.) l_j is formed from x c as well, so rows whose m c is
+// large (at the extreme, all entries at the lowest finite value) take their
+// differences from m first: base = m, else 0.
 struct GradRow {
   float low;         // bound of x - base
-  float ki, mk;      // ki, 1.5 * 2^23 - ki
-  float k1, k0;      // gradient = 2^f 2^n (k1 u + k0)
+  float mk;          // 1.5 * 2^23 + 64 - ki
+  float k1, k0;      // gradient = 2^f 2^(n + 64) (k1 (x - base) + k0)
+  int32_t target;    // column within the tile, out of [0, 128) if elsewhere
   float add;         // scale dlogp, at the target
   float base;
-  int32_t target;    // column within the tile, out of [0, 128) if elsewhere
-};
-
-struct GradScale {
-  float c, r;
 };
 
 constexpr float kMagic = 12582912.0f;      // 1.5 * 2^23
-constexpr int32_t kMagicBits = 0x4B400000;
+constexpr float kFarRow = 1024.0f;         // |m c| from which base = m
+constexpr double kAt = -16.0;              // log2 p where c's rounding is made up for
 
 template <bool FAR>
-__device__ __forceinline__ float grad_value(float x, const GradRow& g, GradScale c, float add) {
+__device__ __forceinline__ float grad_value(float x, const GradRow& g, float c, float add) {
   const float y = fmaxf(FAR ? x - g.base : x, g.low);
-  const float u = fmaf(y, c.c, -g.ki);
-  const float w = u + kMagic;
-  const float kn = w - g.mk;               // ki + n
-  const float f = fmaf(kn, c.r, fmaf(y, c.c, -kn));
-  const float p = ldexpf(__builtin_amdgcn_exp2f(f), __float_as_int(w) - kMagicBits);
-  return fmaf(p, fmaf(u, g.k1, g.k0), add);
+  const float w = fmaf(y, c, g.mk);
+  const float f = fmaf(y, c, g.mk - w);    // mk - w = -(ki + n), exactly
+  const uint32_t p = __float_as_uint(__builtin_amdgcn_exp2f(f)) + (__float_as_uint(w) << 23);
+  return fmaf(__uint_as_float(p), fmaf(y, g.k1, g.k0), add);
 }
 
 template <bool F32, bool FAR>
-__device__ __forceinline__ uint4 grad_chunk(RawChunk<F32> raw, const GradRow& row, GradScale c, uint32_t col) {
+__device__ __forceinline__ uint4 grad_chunk(RawChunk<F32> raw, const GradRow& row, float c, uint32_t col) {
   // one chunk after the other: left to interleave four of them, the compiler
   // takes 82 VGPRs, too many for a fourth tile on the CU (495 us against 460 at
   // 4096 x 131072)
@@ -632,19 +650,27 @@ __device__ __forceinline__ uint4 grad_chunk(RawChunk<F32> raw, const GradRow& ro
   return v;
 }
 
-template <class F, bool F32, bool FULL>
+// What goes past the Infinity Cache (256 MB) on its way, see launch_logprob_bwd.
+enum GradKind {
+  kGradSmall,    // the row-wise codes
+  kGradLarge,    // and the column-wise ones
+  kGradStream,   // and the logits
+};
+
+template <class F, bool F32, GradKind KIND, bool FULL>
 __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& l, GradRow* rows, int64_t r0, int64_t c0,
                                                  int rows_valid, int rows_pad, int cols_valid, int cols_pad) {
   constexpr int kB = F32 ? 4 : 2;
   const uint32_t t = threadIdx.x, cc = t & 15, tr = t >> 4;
-  const double cd0 = (double)a.scale * kLog2eD;
-  const GradScale c{(float)cd0, (float)((cd0 - (double)(float)cd0) / cd0)};
+  const double cd = (double)a.scale * kLog2eD;
+  const float c = (float)cd;
   const char* base = static_cast<const char*>(a.x) + (r0 * a.ld + c0) * kB;
   RawChunk<F32> raw[kChunks];
 #pragma unroll
   for (int j = 0; j < kChunks; ++j) {
     if constexpr (FULL) {
-      __builtin_memcpy(&raw[j], base + (int64_t)(kRowStep * j) * a.ld * kB + (tr * (uint32_t)a.ld + cc * 8) * kB, sizeof(raw[j]));
+      raw[j] = load_raw<F32, KIND == kGradStream>(base + (int64_t)(kRowStep * j) * a.ld * kB +
+                                                  (tr * (uint32_t)a.ld + cc * 8) * kB);
     } else {
       float f[8];
       const int row = tr + kRowStep * j;
@@ -660,7 +686,7 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
   bool row_far = false;
   if ((int)t < kTR) {
     GradRow g{};
-    g.mk = kMagic;
+    g.mk = kMagic + 64.0f;
     g.target = -1;
     if (FULL || (int)t < rows_valid) {
       const int64_t row = r0 + t;
@@ -668,21 +694,20 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
       const int64_t tg = row_target(a, row);
       if (c0 == 0 && a.dev_err && tg < 0 && a.targets[row] != a.ignore_index) atomicOr(a.dev_err, 8);
       if (!(m == -INFINITY && ls == -INFINITY)) {   // a row with nothing left has gradient 0
-        const double cd = (double)a.scale * kLog2eD;
-        row_far = !(fabsf(m) * (float)cd <= 1048576.0f);
+        row_far = !(fabsf(m) * c <= kFarRow);
         const float d = tg >= 0 && a.dlogp ? a.dlogp[row] : 0.0f;
         const float dent = a.dent ? a.dent[row] : 0.0f;
-        const double K = fma(row_far ? 0.0 : (double)m, cd, (double)ls * kLog2eD);
-        const double ki = rint(K);
-        const float kf = (float)(K - ki);
-        const float fold = __builtin_amdgcn_exp2f(-kf);
-        const float k1 = -a.scale * kLn2 * dent;
-        const float k0 = fmaf(-k1, kf, -a.scale * (a.dent ? fmaf(dent, a.ent_in[row], d) : d));
-        g.ki = (float)ki;
-        g.low = (g.ki - 160.0f) / c.c;
-        g.mk = kMagic - g.ki;
-        g.k1 = k1 * fold;
-        g.k0 = k0 * fold;
+        double K = fma(row_far ? 0.0 : (double)m, cd, (double)ls * kLog2eD);
+        K -= (K + kAt) * ((cd - (double)c) / cd);
+        const double ki = rint(K), kf = K - ki;
+        const float fold = __builtin_amdgcn_exp2f((float)-kf) * 0x1p-64f;
+        const double k1 = -(double)a.scale * a.scale * dent;   // times y: scale dent l_j up to a constant
+        const double l0 = -((double)ls + (row_far ? 0.0 : (double)m * a.scale));   // l_j at y = 0
+        const double k0 = -(double)a.scale * (a.dent ? fma((double)dent, (double)a.ent_in[row] + l0, (double)d) : (double)d);
+        g.low = ((float)ki - 186.0f) / c;
+        g.mk = kMagic + 64.0f - (float)ki;
+        g.k1 = (float)k1 * fold;
+        g.k0 = (float)k0 * fold;
         g.base = row_far ? m : 0.0f;
         g.add = a.scale * d;
         g.target = tg >= c0 && tg < c0 + kTC ? (int32_t)(tg - c0) : -1;
@@ -708,11 +733,12 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
       for (int k = 0; k < 4; ++k) w[k] = left >= 2 * k + 2 ? w[k] : left == 2 * k + 1 ? w[k] & 0xFFFFu : 0u;
     }
   }
-  fmt_dual<F, FULL>(v, l, rows_valid, rows_pad, cols_pad, TileOut{a.q_row, a.s_row, a.vocab_pad, a.rows, F::k128},
-                    TileOut{a.q_col, a.s_col, a.rows_pad, a.vocab_pad, F::k128}, r0, c0, false);
+  fmt_dual<F, FULL, true, KIND != kGradSmall>(v, l, rows_valid, rows_pad, cols_pad,
+                                 TileOut{a.q_row, a.s_row, a.vocab_pad, a.rows, F::k128},
+                                 TileOut{a.q_col, a.s_col, a.rows_pad, a.vocab_pad, F::k128}, r0, c0, false);
 }
 
-template <class F, bool F32>
+template <class F, bool F32, GradKind KIND>
 __global__ __launch_bounds__(kFmtThreads, F32 ? 6 : 8) void k_logprob_bwd(LogprobArgs a) {
   __shared__ TileLds l;
   __shared__ GradRow rows[kTR];
@@ -724,9 +750,9 @@ __global__ __launch_bounds__(kFmtThreads, F32 ? 6 : 8) void k_logprob_bwd(Logpro
   const int cols_valid = (int)min<int64_t>(kTC, a.vocab - c0);
   const int cols_pad = (int)min<int64_t>(kTC, a.vocab_pad - c0);
   if (rows_valid == kTR && cols_valid == kTC)
-    logprob_bwd_tile<F, F32, true>(a, l, rows, r0, c0, kTR, kTR, kTC, kTC);
+    logprob_bwd_tile<F, F32, KIND, true>(a, l, rows, r0, c0, kTR, kTR, kTC, kTC);
   else
-    logprob_bwd_tile<F, F32, false>(a, l, rows, r0, c0, rows_valid, rows_pad, cols_valid, cols_pad);
+    logprob_bwd_tile<F, F32, KIND, false>(a, l, rows, r0, c0, rows_valid, rows_pad, cols_valid, cols_pad);
 }
 
 // ---------------------------------------------------------------- launch
@@ -751,6 +777,11 @@ static Split split_rows(int64_t rows, int64_t vocab) {
 // 6.9 against 7.4).
 static bool wide_groups(int64_t groups, int64_t seg) { return groups <= 256 && seg >= 32768; }
 
+// Logits that the Infinity Cache (256 MB) cannot hold are not kept there: 4096 x
+// 131072 197 -> 192 us, 3000 x 50001 76 -> 74.6 (200 x 131072, which it can hold,
+// 17.7 -> 19.8 where it does).
+static bool past_caches(const LogprobArgs& a) { return a.rows * a.vocab * (a.f32 ? 4 : 2) > (1ll << 28); }
+
 int64_t logprob_work(int64_t rows, int64_t vocab, int32_t top) {
   const Split sp = split_rows(rows, vocab);
   return sp.parts == 1 ? 0 : soft_bytes(rows, sp.parts) + rows * sp.parts * top * (int64_t)sizeof(uint64_t);
@@ -761,9 +792,11 @@ static hipError_t launch_fwd(const LogprobArgs& a, hipStream_t s) {
   const Split sp = split_rows(a.rows, a.vocab);
   const dim3 grid((unsigned)(a.rows * sp.parts));
   if (wide_groups(a.rows * sp.parts, sp.seg))
-    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 512>), grid, dim3(512), 0, s, a, sp);
+    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 512, false>), grid, dim3(512), 0, s, a, sp);
+  else if (past_caches(a))
+    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 256, true>), grid, dim3(256), 0, s, a, sp);
   else
-    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 256>), grid, dim3(256), 0, s, a, sp);
+    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 256, false>), grid, dim3(256), 0, s, a, sp);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || sp.parts == 1) return e;
   hipLaunchKernelGGL((k_logprob_join<F32, TOP>), dim3((unsigned)a.rows), dim3(kJoinThreads), 0, s, a, sp);
@@ -781,9 +814,33 @@ hipError_t launch_logprob_fwd(const LogprobArgs& a, hipStream_t s) {
 // 4096 x 50304 float32 265 -> 248; without it smaller gradients are faster
 // (8192 x 16384 116 against 132 us, 2048 x 131072 float32 310 against 327), and
 // so are unaligned rows (6000 x 100001 489 against 528).
+static bool aligned_rows(const LogprobArgs& a) {
+  return a.ld * (a.f32 ? 4 : 2) % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
+}
+
 static bool grad_bands(const LogprobArgs& a, int64_t nx, int64_t ny) {
-  const int64_t pitch = a.ld * (a.f32 ? 4 : 2);
-  return nx * ny >= 48 * 256 && ny >= 32 && pitch % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
+  return nx * ny >= 48 * 256 && ny >= 32 && aligned_rows(a);
+}
+
+// Where each direction's codes are past what the 256 MB Infinity Cache can hold
+// for the head's gradient GEMMs, both go past it: 4096 x 131072 456 -> 445 us;
+// and so do the logits, read here for the last time, where no line is shared by
+// two tiles: 445 -> 429 (6000 x 100001, unaligned, 588 against 605 with them).
+// Below that size only the row-wise codes do: 333 x 50001 float32 28.2 -> 27.2
+// us; with both 26.4, but the two GEMMs behind it then take 3 us longer (7 us
+// behind 1000 x 32000).
+static GradKind grad_kind(const LogprobArgs& a) {
+  if (a.rows_pad * a.vocab_pad <= (1ll << 28)) return kGradSmall;
+  return aligned_rows(a) ? kGradStream : kGradLarge;
+}
+
+template <class F, bool F32>
+static void launch_bwd(const LogprobArgs& a, dim3 grid, hipStream_t s) {
+  switch (grad_kind(a)) {
+    case kGradSmall: hipLaunchKernelGGL((k_logprob_bwd<F, F32, kGradSmall>), grid, dim3(kFmtThreads), 0, s, a); break;
+    case kGradLarge: hipLaunchKernelGGL((k_logprob_bwd<F, F32, kGradLarge>), grid, dim3(kFmtThreads), 0, s, a); break;
+    case kGradStream: hipLaunchKernelGGL((k_logprob_bwd<F, F32, kGradStream>), grid, dim3(kFmtThreads), 0, s, a); break;
+  }
 }
 
 hipError_t launch_logprob_bwd(const LogprobArgs& args, hipStream_t s) {
@@ -792,8 +849,8 @@ hipError_t launch_logprob_bwd(const LogprobArgs& args, hipStream_t s) {
   a.bands = grad_bands(a, nx, ny);
   const dim3 grid((unsigned)(nx * ny));
   with_fmt(a.rceil, a.k128, [&](auto f) {
-    if (a.f32) hipLaunchKernelGGL((k_logprob_bwd<decltype(f), true>), grid, dim3(kFmtThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_logprob_bwd<decltype(f), false>), grid, dim3(kFmtThreads), 0, s, a);
+    if (a.f32) launch_bwd<decltype(f), true>(a, grid, s);
+    else launch_bwd<decltype(f), false>(a, grid, s);
   });
   return hipGetLastError();
 }

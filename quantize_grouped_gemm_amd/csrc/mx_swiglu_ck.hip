@@ -8,6 +8,12 @@
 // input is read once into registers, everything else happens on chip. Rows
 // past the last one enter as zeros, so the column-wise blocks that they fill
 // up quantize to zeros.
+//
+// Both are bound by HBM. Stores: the checkpoint is read in the backward pass
+// only and goes past the caches (8192 x 14336 forward 197 -> 167..186 us); of
+// the backward's two outputs, 480 MB at that size, the Infinity Cache can hold
+// one, so the row-wise one goes past it, and so do the checkpoint's codes,
+// read for the last time (197 -> 172 us; both outputs past it 188).
 
 #include "mx_device.h"
 #include "mx_fmt.h"
@@ -24,13 +30,13 @@ __device__ __forceinline__ void swiglu_ck_fwd_tile(const SwigluCkArgs& a, TileLd
   fmt_load<FULL>(v, a.a + r0 * a.ld_ab + c0, a.ld_ab, rows_valid, cols_valid);
   fmt_load<FULL>(w, a.b + r0 * a.ld_ab + c0, a.ld_ab, rows_valid, cols_valid);
   const TileOut ock{a.q_ck, a.s_ck, 2 * a.hidden, a.rows, F::k128};
-  fmt_rowq<F, FULL>(v, rows_valid, cols_valid, ock, r0, c0, s_ck[0]);
-  fmt_rowq<F, FULL>(w, rows_valid, cols_valid, ock, r0, a.hidden + c0, s_ck[1]);
+  fmt_rowq<F, FULL, true>(v, rows_valid, cols_valid, ock, r0, c0, s_ck[0]);
+  fmt_rowq<F, FULL, true>(w, rows_valid, cols_valid, ock, r0, a.hidden + c0, s_ck[1]);
 #pragma unroll
   for (int j = 0; j < kChunks; ++j)
     v[j] = make_uint4(swiglu_pair(v[j].x, w[j].x), swiglu_pair(v[j].y, w[j].y),
                       swiglu_pair(v[j].z, w[j].z), swiglu_pair(v[j].w, w[j].w));
-  fmt_dual<F, FULL>(v, l, rows_valid, rows_pad, cols_valid, TileOut{a.q_row, a.s_row, a.hidden, a.rows, F::k128},
+  fmt_dual<F, FULL, false, false>(v, l, rows_valid, rows_pad, cols_valid, TileOut{a.q_row, a.s_row, a.hidden, a.rows, F::k128},
                     TileOut{a.q_col, a.s_col, a.rows_pad, a.hidden, F::k128}, r0, c0, false);
   const int t = threadIdx.x & (kTR - 1), half = (int)threadIdx.x / kTR - 2;   // the threads that fmt_dual leaves idle
   if (half >= 0) fmt_scales<F>(s_ck[half], t, rows_valid, cols_valid, ock, r0, half * a.hidden + c0);
@@ -70,10 +76,10 @@ __device__ __forceinline__ void tile_load_codes(uint2 (&q)[kChunks], uint32_t (&
   for (int j = 0; j < kChunks; ++j) {
     const uint32_t r = FULL ? (t >> 4) + kRowStep * j : (uint32_t)min((int)(t >> 4) + kRowStep * j, rows_valid - 1);
     if constexpr (FULL) {
-      q[j] = *reinterpret_cast<const uint2*>(qbase + (int64_t)(kRowStep * j) * ld + ((t >> 4) * (uint32_t)ld + c));
+      q[j] = load_stream8(qbase + (int64_t)(kRowStep * j) * ld + ((t >> 4) * (uint32_t)ld + c));
       sb[j] = sbase[(int64_t)(kRowStep * j) * sld + ((t >> 4) * sld + (c >> 5))];
     } else {
-      q[j] = *reinterpret_cast<const uint2*>(qbase + r * ld + c);
+      q[j] = load_stream8(qbase + r * ld + c);
       sb[j] = sbase[(int64_t)r * sld + (c >> 5)];
     }
   }
@@ -111,8 +117,8 @@ __device__ __forceinline__ void swiglu_ck_bwd_tile(const SwigluCkArgs& a, TileLd
   }
   const TileOut orow{a.q_row, a.s_row, H2, a.rows, F::k128};
   const TileOut ocol{a.q_col, a.s_col, a.rows_pad, H2, F::k128};
-  fmt_dual<F, FULL>(da, l, rows_valid, rows_pad, cols_valid, orow, ocol, r0, c0, true);
-  fmt_dual<F, FULL>(db, l, rows_valid, rows_pad, cols_valid, orow, ocol, r0, a.hidden + c0, false);
+  fmt_dual<F, FULL, true, false>(da, l, rows_valid, rows_pad, cols_valid, orow, ocol, r0, c0, true);
+  fmt_dual<F, FULL, true, false>(db, l, rows_valid, rows_pad, cols_valid, orow, ocol, r0, a.hidden + c0, false);
 }
 
 template <class F>
