@@ -28,6 +28,13 @@ struct Fmt {
   static constexpr bool rceil = RCEIL, k128 = K128;
 };
 
+// n rounded up to the layout's block step.
+template <class F>
+__device__ __forceinline__ int64_t padded(int64_t n) {
+  constexpr int64_t step = F::k128 ? 128 : kBlock;
+  return (n + step - 1) / step * step;
+}
+
 constexpr int kFmtThreads = 512;
 constexpr int kChunks = kTR * kTC / 8 / kFmtThreads;   // 4 per thread
 constexpr int kRowStep = kFmtThreads / 16;              // rows between a thread's chunks

@@ -29,26 +29,27 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr double kLog2eD = 1.4426950408889634074;
 constexpr float kLn2 = 0.693147180559945309f;
 
-// 8 logits starting at element `i` of a row of n; `fill` past the end.
-template <bool F32>
-__device__ __forceinline__ void load_logits(const void* row, int64_t i, int64_t n, float fill, float (&f)[8]) {
+// N logits starting at element `i` < n of a row of n; `fill` past the end.
+template <bool F32, int N>
+__device__ __forceinline__ void load_logits(const void* row, int64_t i, int64_t n, float fill, float (&f)[N]) {
   if constexpr (F32) {
     const float* p = static_cast<const float*>(row) + i;
-    if (i + 8 <= n) {
-      __builtin_memcpy(f, p, 32);
+    if (i + N <= n) {
+      __builtin_memcpy(f, p, 4 * N);
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = i + k < n ? p[k] : fill;
+      for (int k = 0; k < N; ++k) f[k] = i + k < n ? p[k] : fill;
     }
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(row) + i;
-    if (i + 8 <= n) {
-      uint4 v;
-      __builtin_memcpy(&v, p, 16);
-      unpack8(v, f);
+    if (i + N <= n) {
+      uint16_t v[N];
+      __builtin_memcpy(v, p, 2 * N);
+#pragma unroll
+      for (int k = 0; k < N; ++k) f[k] = __uint_as_float((uint32_t)v[k] << 16);
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = i + k < n ? __uint_as_float((uint32_t)p[k] << 16) : fill;
+      for (int k = 0; k < N; ++k) f[k] = i + k < n ? __uint_as_float((uint32_t)p[k] << 16) : fill;
     }
   }
 }
@@ -57,6 +58,52 @@ template <bool F32>
 __device__ __forceinline__ const void* logits_row(const LogprobArgs& a, int64_t row) {
   return static_cast<const char*>(a.x) + row * a.ld * (F32 ? 4 : 2);
 }
+
+// Arguments of the forward kernels; part_work and the rest see them widened.
+struct LogprobPack {
+  const void* x;
+  const int64_t* targets;
+  int32_t* dev_err;
+  float *logp, *entropy, *stats, *top_logp;
+  int32_t* top_idx;
+  void* work;
+  int64_t ignore_index, ld;
+  int32_t rows, vocab, top;
+  float scale;
+  int32_t parts, seg;        // of a row's split
+
+  __device__ LogprobArgs wide() const {
+    LogprobArgs a{};
+    a.x = x; a.ld = ld; a.rows = rows; a.vocab = vocab; a.targets = targets; a.ignore_index = ignore_index;
+    a.scale = scale; a.dev_err = dev_err; a.top = top; a.logp = logp; a.entropy = entropy; a.stats_out = stats;
+    a.top_logp = top_logp; a.top_idx = top_idx; a.work = work;
+    return a;
+  }
+};
+static_assert(sizeof(LogprobPack) <= kArgBytes);
+
+struct LogprobBwdPack {
+  const void* x;
+  const int64_t* targets;
+  int32_t* dev_err;
+  const float *stats, *ent_in, *dlogp, *dent;
+  uint8_t *q_row, *s_row, *q_col, *s_col;
+  int64_t ignore_index;
+  uint32_t ld_bands;         // 2 ld + bands
+  int32_t rows, vocab;
+  float scale;
+
+  template <class F>
+  __device__ LogprobArgs wide() const {
+    LogprobArgs a{};
+    a.x = x; a.ld = ld_bands >> 1; a.bands = ld_bands & 1; a.rows = rows; a.vocab = vocab; a.targets = targets;
+    a.ignore_index = ignore_index; a.scale = scale; a.dev_err = dev_err; a.stats = stats; a.ent_in = ent_in;
+    a.dlogp = dlogp; a.dent = dent; a.vocab_pad = padded<F>(vocab); a.rows_pad = padded<F>(rows);
+    a.q_row = q_row; a.s_row = s_row; a.q_col = q_col; a.s_col = s_col;
+    return a;
+  }
+};
+static_assert(sizeof(LogprobBwdPack) <= kArgBytes);
 
 // The row's target, or -1 if it is not scored.
 __device__ __forceinline__ int64_t row_target(const LogprobArgs& a, int64_t row) {
@@ -149,6 +196,7 @@ template <bool F32>
 constexpr int kUnroll = F32 ? 2 : 4;
 
 __device__ __forceinline__ uint32_t key16(float x) { return (uint32_t)(top_key(x, 0) >> 48); }
+constexpr uint32_t kLowest16 = 0x007F;      // key16(-infinity), no other value's
 
 template <int N>
 __device__ __forceinline__ float max_of(const float (&f)[N], float m) {
@@ -177,6 +225,7 @@ struct TopLds {
   uint64_t thr;          // entries with a larger key are candidates
   uint16_t list[kList];
   uint16_t tkey[NT];
+  bool any[2][NT / 64];
   int count, hits;
 };
 
@@ -205,22 +254,6 @@ __device__ __forceinline__ void keep_top(TopLds<NT>& l, int top) {
   __syncthreads();
 }
 
-// Offers up to kRound / NT entries of a thread: those above the threshold
-// become candidates.
-template <bool F32, int NT>
-__device__ __forceinline__ void offer(TopLds<NT>& l, const void* x, int64_t i, int64_t n, uint32_t idx0) {
-  const uint64_t thr = l.thr;
-#pragma unroll
-  for (int k = 0; k < kRound / NT; ++k) {
-    if (i + k < n) {
-      const float f = F32 ? static_cast<const float*>(x)[i + k]
-                          : __uint_as_float((uint32_t)static_cast<const uint16_t*>(x)[i + k] << 16);
-      const uint64_t key = top_key(f, idx0 + (uint32_t)(i + k));
-      if (key > thr) l.cand[atomicAdd(&l.count, 1)] = key;
-    }
-  }
-}
-
 // Between two rounds of offers: makes room if the next one might not fit. All
 // threads call it.
 template <int NT>
@@ -231,16 +264,111 @@ __device__ __forceinline__ void make_room(TopLds<NT>& l, int top) {
   else __syncthreads();
 }
 
+// Offers N consecutive entries of a thread from index i on: those of keys above
+// thr become candidates (those past kCand are only counted).
+template <bool F32, int N, int NT>
+__device__ __forceinline__ void offer(TopLds<NT>& l, const void* x, int64_t i, int64_t n, uint32_t idx0, uint64_t thr) {
+  float f[N];
+  load_logits<F32>(x, i, n, -INFINITY, f);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint64_t key = top_key(f[k], idx0 + (uint32_t)(i + k));
+    if (key > thr && i + k < n) {
+      const int at = atomicAdd(&l.count, 1);
+      if (at < kCand) l.cand[at] = key;
+    }
+  }
+}
+
+// Lists the slots whose maximum is at least `bound`; returns their number (all
+// threads call it, barriers inside).
+template <int NT>
+__device__ __forceinline__ int list_slots(TopLds<NT>& l, int slots, uint32_t bound) {
+  const int t = threadIdx.x;
+  __syncthreads();
+  if (t == 0) l.hits = 0;
+  __syncthreads();
+  for (int s = 0; s < slots; ++s) {
+    if (l.slot[s][t] >= bound) {
+      const int at = atomicAdd(&l.hits, 1);
+      if (at < kList) l.list[at] = (uint16_t)(s * NT + t);
+    }
+  }
+  __syncthreads();
+  return l.hits;
+}
+
+// Candidates from the listed slots: entries of keys above thr. No barriers
+// between its loads: few entries pass, and if more do than there is room for,
+// l.count says so afterwards.
+template <bool F32, int NT>
+__device__ __forceinline__ void offer_list(TopLds<NT>& l, const void* x, int64_t n, uint32_t idx0, int hits, int tiles,
+                                           uint64_t thr) {
+  constexpr int kEach = kRound / NT, kSplit = 8 / kEach;   // entries at a time, pieces of a chunk
+  const int per = kUnroll<F32> * tiles;                    // chunks of a slot
+  for (int item = threadIdx.x; item < hits * per * kSplit; item += NT) {
+    const int e = l.list[item / (per * kSplit)], h = item % (per * kSplit);
+    const int64_t i = 8 * ((int64_t)(e / NT) * per * NT + (int64_t)(h / kSplit) * NT + e % NT) + kEach * (h % kSplit);
+    if (i < n) offer<F32, kEach, NT>(l, x, i, n, idx0, thr);
+  }
+  __syncthreads();
+}
+
+// Candidates from the whole segment, read again: first one entry a thread, whose
+// best raise the threshold, then in pieces that cost a barrier where nothing
+// passes.
+template <bool F32, int NT>
+__device__ __forceinline__ void offer_all(TopLds<NT>& l, const void* x, int64_t n, uint32_t idx0, int top) {
+  constexpr int kEach = kRound / NT, kPiece = 8 * kRound;
+  const int t = threadIdx.x;
+  __syncthreads();
+  if (t == 0) l.count = 0;
+  __syncthreads();
+  if (t < n) offer<F32, 1, NT>(l, x, t, n, idx0, l.thr);
+  keep_top(l, top);
+  for (int64_t base = NT; base < n; base += kPiece) {
+    const uint64_t thr = l.thr;
+    bool any = false;
+    for (int j = 0; j < 8; ++j) {
+      const int64_t i = base + (int64_t)kRound * j + kEach * t;
+      float f[kEach];
+      if (i < n) {
+        load_logits<F32>(x, i, n, -INFINITY, f);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) any |= top_key(f[k], idx0 + (uint32_t)(i + k)) > thr && i + k < n;
+      }
+    }
+    const int turn = (int)(base / kPiece) & 1;   // the other one may still be read
+    any = __any(any);
+    if ((t & 63) == 0) l.any[turn][t >> 6] = any;
+    __syncthreads();
+    any = false;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) any |= l.any[turn][w];
+    if (!__builtin_amdgcn_readfirstlane(any)) continue;
+    for (int j = 0; j < 8; ++j) {
+      const int64_t i = base + (int64_t)kRound * j + kEach * t;
+      if (i < n) offer<F32, kEach, NT>(l, x, i, n, idx0, l.thr);
+      make_room(l, top);
+    }
+  }
+}
+
 // The `top` best entries of the segment [0, n) of x (first index idx0), in
 // descending order in l.cand[0 .. l.count). `slots` slots of `tiles` tiles
 // each; tmax the thread's maximum.
+//
+// Where most slots reach the bound, a mask (or a constant) has made it the
+// value of most entries. If equal upper halves of float32 mean equal values (bf16, and
+// -infinity in either type), the entries above it come from the few slots above it, and
+// the others are the first ones in order of their index.
 template <bool F32, int NT>
 __device__ __forceinline__ void find_top(TopLds<NT>& l, const void* x, int64_t n, uint32_t idx0, float tmax, int slots,
                                          int tiles, int top) {
-  constexpr int U = kUnroll<F32>;
+  constexpr int kFill = 128;
   const int t = threadIdx.x;
   l.tkey[t] = (uint16_t)key16(tmax);
-  if (t == 0) l.count = l.hits = 0;
+  if (t == 0) l.count = 0;
   __syncthreads();
   if (t < 64) {
     // the top-th largest of the NT keys, bit by bit
@@ -258,35 +386,33 @@ __device__ __forceinline__ void find_top(TopLds<NT>& l, const void* x, int64_t n
     if (t == 0) l.thr = bound ? ((uint64_t)bound << 48) - 1 : 0;
   }
   __syncthreads();
-  const uint32_t bound = (uint32_t)((l.thr + 1) >> 48);
-  for (int s = 0; s < slots; ++s) {
-    if (l.slot[s][t] >= bound) {
-      const int at = atomicAdd(&l.hits, 1);
-      if (at < kList) l.list[at] = (uint16_t)(s * NT + t);
-    }
-  }
-  __syncthreads();
-  const int hits = l.hits;
-  constexpr int kEach = kRound / NT;           // entries per thread and round
-  const int per = 8 / kEach * U * tiles;       // such pieces of a slot
-  const int64_t items = (int64_t)hits * per;
-  if (hits <= kList) {
-    for (int64_t base = 0; base < items; base += NT) {
-      const int item = (int)base + t;
-      if (item < items) {
-        const int e = l.list[item / per], h = item % per;
-        const int64_t chunk = ((int64_t)(e / NT) * tiles * U + h / (8 / kEach)) * NT + e % NT;
-        offer<F32, NT>(l, x, 8 * chunk + kEach * (h % (8 / kEach)), n, idx0);
+  int hits = list_slots(l, slots, (uint32_t)((l.thr + 1) >> 48));
+  const uint64_t thr = l.thr;
+  const uint32_t bound = (uint32_t)((thr + 1) >> 48);
+  bool whole = true;
+  if (2 * hits > slots * NT && (!F32 || bound == kLowest16)) {
+    hits = list_slots(l, slots, bound + 1);
+    if (hits <= kList) {
+      offer_list<F32, NT>(l, x, n, idx0, hits, tiles, thr + (1ull << 48));
+      whole = l.count > kCand;
+      // a few at a time, as most are of that value: ranking takes the square of their number
+      for (int64_t base = 0; !whole && l.count < top && base < n; base += kFill) {
+        __syncthreads();
+        const int64_t i = base + t;
+        if (t < kFill && i < n) {
+          float f[1];
+          load_logits<F32>(x, i, n, -INFINITY, f);
+          const uint64_t key = top_key(f[0], idx0 + (uint32_t)i);
+          if ((uint32_t)(key >> 48) == bound) l.cand[atomicAdd(&l.count, 1)] = key;
+        }
+        __syncthreads();
       }
-      if (items * kEach > kCand) make_room(l, top);
     }
-  } else {
-    // so many slots qualify (equal or sorted entries): read the segment again
-    for (int64_t base = 0; base < n; base += kRound) {
-      offer<F32, NT>(l, x, base + kEach * t, n, idx0);
-      make_room(l, top);
-    }
+  } else if (hits <= kList) {
+    offer_list<F32, NT>(l, x, n, idx0, hits, tiles, thr);
+    whole = l.count > kCand;
   }
+  if (whole) offer_all<F32, NT>(l, x, n, idx0, top);
   keep_top(l, top);
 }
 
@@ -394,7 +520,9 @@ __device__ __forceinline__ PartWork part_work(const LogprobArgs& a, const Split&
 }
 
 template <bool F32, bool TOP, int NT, bool STREAM>
-__global__ __launch_bounds__(NT) void k_logprob_part(LogprobArgs a, Split sp) {
+__global__ __launch_bounds__(NT) void k_logprob_part(LogprobPack pack) {
+  const LogprobArgs a = pack.wide();
+  const Split sp{pack.parts, pack.seg};
   constexpr int U = kUnroll<F32>;
   constexpr int kTile = 8 * U * NT, kWaves = NT / 64;
   __shared__ float red[3][kWaves];
@@ -529,7 +657,9 @@ __global__ __launch_bounds__(NT) void k_logprob_part(LogprobArgs a, Split sp) {
 // below; what reaches it, rarely many more than `top`, is ranked. All loads of
 // global memory are issued at the start: the kernel is a chain of latencies.
 template <bool F32, bool TOP>
-__global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobArgs a, Split sp) {
+__global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobPack pack) {
+  const LogprobArgs a = pack.wide();
+  const Split sp{pack.parts, pack.seg};
   const int t = threadIdx.x, lane = t & 63;
   const int64_t row = blockIdx.x;
   const PartWork w = part_work(a, sp);
@@ -658,8 +788,8 @@ enum GradKind {
 };
 
 template <class F, bool F32, GradKind KIND, bool FULL>
-__device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& l, GradRow* rows, int64_t r0, int64_t c0,
-                                                 int rows_valid, int rows_pad, int cols_valid, int cols_pad) {
+__device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& l, GradRow* rows, bool* far_rows,
+                                                 int64_t r0, int64_t c0, int rows_valid, int rows_pad, int cols_valid, int cols_pad) {
   constexpr int kB = F32 ? 4 : 2;
   const uint32_t t = threadIdx.x, cc = t & 15, tr = t >> 4;
   const double cd = (double)a.scale * kLog2eD;
@@ -715,7 +845,12 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
     }
     rows[t] = g;
   }
-  const bool far = __syncthreads_or(row_far);
+  if ((int)t < kTR) {
+    const bool any = __any(row_far);
+    if ((t & 63) == 0) far_rows[t >> 6] = any;
+  }
+  __syncthreads();
+  const bool far = __builtin_amdgcn_readfirstlane(far_rows[0] | far_rows[1]);
   uint4 v[kChunks];
   if (!far) {
 #pragma unroll
@@ -739,9 +874,11 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
 }
 
 template <class F, bool F32, GradKind KIND>
-__global__ __launch_bounds__(kFmtThreads, F32 ? 6 : 8) void k_logprob_bwd(LogprobArgs a) {
+__global__ __launch_bounds__(kFmtThreads, F32 ? 6 : 8) void k_logprob_bwd(LogprobBwdPack pack) {
   __shared__ TileLds l;
   __shared__ GradRow rows[kTR];
+  __shared__ bool far_rows[kTR / 64];
+  const LogprobArgs a = pack.wide<F>();
   const TilePos at = tile_pos(blockIdx.x, (uint32_t)((a.vocab_pad + kTC - 1) / kTC), (uint32_t)((a.rows_pad + kTR - 1) / kTR),
                               a.bands);
   const int64_t r0 = at.r0, c0 = at.c0;
@@ -750,9 +887,9 @@ __global__ __launch_bounds__(kFmtThreads, F32 ? 6 : 8) void k_logprob_bwd(Logpro
   const int cols_valid = (int)min<int64_t>(kTC, a.vocab - c0);
   const int cols_pad = (int)min<int64_t>(kTC, a.vocab_pad - c0);
   if (rows_valid == kTR && cols_valid == kTC)
-    logprob_bwd_tile<F, F32, KIND, true>(a, l, rows, r0, c0, kTR, kTR, kTC, kTC);
+    logprob_bwd_tile<F, F32, KIND, true>(a, l, rows, far_rows, r0, c0, kTR, kTR, kTC, kTC);
   else
-    logprob_bwd_tile<F, F32, KIND, false>(a, l, rows, r0, c0, rows_valid, rows_pad, cols_valid, cols_pad);
+    logprob_bwd_tile<F, F32, KIND, false>(a, l, rows, far_rows, r0, c0, rows_valid, rows_pad, cols_valid, cols_pad);
 }
 
 // ---------------------------------------------------------------- launch
@@ -791,15 +928,18 @@ template <bool F32, bool TOP>
 static hipError_t launch_fwd(const LogprobArgs& a, hipStream_t s) {
   const Split sp = split_rows(a.rows, a.vocab);
   const dim3 grid((unsigned)(a.rows * sp.parts));
+  const LogprobPack p{a.x, a.targets, a.dev_err, a.logp, a.entropy, a.stats_out, a.top_logp, a.top_idx, a.work,
+                      a.ignore_index, a.ld, (int32_t)a.rows, (int32_t)a.vocab, a.top, a.scale, sp.parts,
+                      (int32_t)sp.seg};
   if (wide_groups(a.rows * sp.parts, sp.seg))
-    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 512, false>), grid, dim3(512), 0, s, a, sp);
+    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 512, false>), grid, dim3(512), 0, s, p);
   else if (past_caches(a))
-    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 256, true>), grid, dim3(256), 0, s, a, sp);
+    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 256, true>), grid, dim3(256), 0, s, p);
   else
-    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 256, false>), grid, dim3(256), 0, s, a, sp);
+    hipLaunchKernelGGL((k_logprob_part<F32, TOP, 256, false>), grid, dim3(256), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || sp.parts == 1) return e;
-  hipLaunchKernelGGL((k_logprob_join<F32, TOP>), dim3((unsigned)a.rows), dim3(kJoinThreads), 0, s, a, sp);
+  hipLaunchKernelGGL((k_logprob_join<F32, TOP>), dim3((unsigned)a.rows), dim3(kJoinThreads), 0, s, p);
   return hipGetLastError();
 }
 
@@ -836,10 +976,13 @@ static GradKind grad_kind(const LogprobArgs& a) {
 
 template <class F, bool F32>
 static void launch_bwd(const LogprobArgs& a, dim3 grid, hipStream_t s) {
+  const LogprobBwdPack p{a.x, a.targets, a.dev_err, a.stats, a.ent_in, a.dlogp, a.dent, a.q_row, a.s_row, a.q_col,
+                         a.s_col, a.ignore_index, (uint32_t)(2 * a.ld + a.bands), (int32_t)a.rows, (int32_t)a.vocab,
+                         a.scale};
   switch (grad_kind(a)) {
-    case kGradSmall: hipLaunchKernelGGL((k_logprob_bwd<F, F32, kGradSmall>), grid, dim3(kFmtThreads), 0, s, a); break;
-    case kGradLarge: hipLaunchKernelGGL((k_logprob_bwd<F, F32, kGradLarge>), grid, dim3(kFmtThreads), 0, s, a); break;
-    case kGradStream: hipLaunchKernelGGL((k_logprob_bwd<F, F32, kGradStream>), grid, dim3(kFmtThreads), 0, s, a); break;
+    case kGradSmall: hipLaunchKernelGGL((k_logprob_bwd<F, F32, kGradSmall>), grid, dim3(kFmtThreads), 0, s, p); break;
+    case kGradLarge: hipLaunchKernelGGL((k_logprob_bwd<F, F32, kGradLarge>), grid, dim3(kFmtThreads), 0, s, p); break;
+    case kGradStream: hipLaunchKernelGGL((k_logprob_bwd<F, F32, kGradStream>), grid, dim3(kFmtThreads), 0, s, p); break;
   }
 }
 

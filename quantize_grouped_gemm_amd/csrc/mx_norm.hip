@@ -28,9 +28,11 @@ struct RowShape {
   int waves, groups, nch;
 };
 
+__host__ __device__ inline int row_groups(int waves) { return waves >= 4 ? 1 : 4 / waves; }
+
 static RowShape row_shape(int64_t cols, int nch) {
   const int waves = (int)((cols + 512 * nch - 1) / (512 * nch));
-  return RowShape{waves, std::max(1, 4 / waves), nch};
+  return RowShape{waves, row_groups(waves), nch};
 }
 
 // Where this thread works: its group's index in the grid, its place in the row.
@@ -43,8 +45,7 @@ struct RowPlace {
 __device__ __forceinline__ RowPlace row_place(int waves) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = w / waves;
-  const int groups = (int)(blockDim.x >> 6) / waves;
-  return RowPlace{(int64_t)blockIdx.x * groups + g, (uint32_t)(threadIdx.x - 64 * g * waves), (uint32_t)(64 * waves),
+  return RowPlace{(int64_t)blockIdx.x * row_groups(waves) + g, (uint32_t)(threadIdx.x - 64 * g * waves), (uint32_t)(64 * waves),
                   g * waves};
 }
 
@@ -63,9 +64,30 @@ __device__ __forceinline__ T group_sum(T v, const RowPlace& p, int waves, T* buf
   return v;
 }
 
+struct NormRowPack {
+  const uint16_t *x, *r;
+  const float* w;
+  uint16_t* sum;
+  float* rstd;
+  uint8_t *q_row, *s_row, *q_ck, *s_ck;
+  int32_t ld_x, ld_r, rows, cols;
+  float eps;
+  int32_t waves;
+
+  __device__ NormFwdArgs wide() const {
+    NormFwdArgs a{};
+    a.x = x; a.r = r; a.w = w; a.ld_x = ld_x; a.ld_r = ld_r; a.rows = rows; a.cols = cols; a.eps = eps;
+    a.sum = sum; a.rstd = rstd; a.q_row = q_row; a.s_row = s_row; a.q_ck = q_ck; a.s_ck = s_ck;
+    return a;
+  }
+};
+static_assert(sizeof(NormRowPack) <= kArgBytes);
+
 template <class F, int NCH>
-__global__ __launch_bounds__(1024) void k_norm_row(NormFwdArgs a, int waves) {
+__global__ __launch_bounds__(1024) void k_norm_row(NormRowPack pack) {
   __shared__ double buf[16];
+  const NormFwdArgs a = pack.wide();
+  const int waves = pack.waves;
   const RowPlace p = row_place(waves);
   const int64_t row = p.group;
   const bool live = row < a.rows;
@@ -133,6 +155,30 @@ static int64_t dw_parts(int64_t rows, int64_t cols) {
   return (rows + r - 1) / r;
 }
 
+struct NormBwdPack {
+  const uint16_t* dy;
+  const void* x;             // x, or the checkpoint's codes
+  const uint8_t* s_ck;
+  const uint16_t* dsum;
+  const float *w, *rstd;
+  uint16_t* dx;
+  uint8_t *q_row, *s_row;
+  float* work;
+  int32_t ld_dy, ld_x, ld_dsum, rows, cols;
+  int16_t waves, per;        // waves and rows of a group
+
+  template <bool CK>
+  __device__ NormBwdArgs wide() const {
+    NormBwdArgs a{};
+    a.dy = dy; a.dsum = dsum; a.w = w; a.rstd = rstd; a.dx = dx; a.q_row = q_row; a.s_row = s_row; a.work = work;
+    if constexpr (CK) { a.q_ck = static_cast<const uint8_t*>(x); a.s_ck = s_ck; }
+    else { a.x = static_cast<const uint16_t*>(x); a.ld_x = ld_x; }
+    a.ld_dy = ld_dy; a.ld_dsum = ld_dsum; a.rows = rows; a.cols = cols;
+    return a;
+  }
+};
+static_assert(sizeof(NormBwdPack) <= kArgBytes);
+
 // What a thread reads of a row.
 template <int NCH, bool CK>
 struct BwdRow {
@@ -170,8 +216,10 @@ __device__ __forceinline__ void bwd_load(BwdRow<NCH, CK>& b, const NormBwdArgs& 
 // it works on one (with one chunk a thread; two would spill); dw's sums over
 // them stay in registers.
 template <class F, int NCH, bool CK>
-__global__ __launch_bounds__(1024) void k_norm_bwd(NormBwdArgs a, int waves, int rows) {
+__global__ __launch_bounds__(1024) void k_norm_bwd(NormBwdPack pack) {
   __shared__ float buf[2][16];
+  const NormBwdArgs a = pack.wide<CK>();
+  const int waves = pack.waves, rows = pack.per;
   const RowPlace p = row_place(waves);
   const int64_t row0 = p.group * rows;
   float dw[NCH][8] = {}, w[NCH][8] = {};
@@ -238,11 +286,12 @@ struct NormTailArgs {
   int64_t ld, rows, rows_pad, cols;
   const float *rstd, *w;     // forward
   uint8_t *q, *s;            // NULL: no column-wise codes
-  int32_t dw_blocks;         // workgroups that join dw, ahead of the tiles
+  int32_t dw_blocks, tiles;  // workgroups that join dw, and the tiles' behind them
   const float* work;
   int64_t parts;
   float* dw;
 };
+static_assert(sizeof(NormTailArgs) <= kArgBytes);
 
 template <class F, bool NORM, bool FULL>
 __device__ __forceinline__ void norm_col_tile(const NormTailArgs& a, TileLds& l, int64_t r0, int64_t c0, int rows_valid,
@@ -300,7 +349,7 @@ __global__ __launch_bounds__(kFmtThreads) void k_norm_tail(NormTailArgs a) {
     join_dw(a, reinterpret_cast<float4*>(l.v));
     return;
   }
-  const uint32_t b = gridDim.x - 1 - blockIdx.x;   // the last tile first
+  const uint32_t b = a.dw_blocks + a.tiles - 1 - blockIdx.x;   // the last tile first
   const uint32_t per_row = (uint32_t)((a.cols + kTC - 1) / kTC);
   const int64_t r0 = (int64_t)(b / per_row) * kTR;
   const int64_t c0 = (int64_t)(b % per_row) * kTC;
@@ -316,9 +365,9 @@ __global__ __launch_bounds__(kFmtThreads) void k_norm_tail(NormTailArgs a) {
 // ---------------------------------------------------------------- launch
 
 template <bool NORM>
-static hipError_t launch_tail(const NormTailArgs& c, bool rceil, bool k128, hipStream_t s) {
-  const int64_t tiles = c.q ? (c.cols + kTC - 1) / kTC * ((c.rows_pad + kTR - 1) / kTR) : 0;
-  const dim3 grid((unsigned)(c.dw_blocks + tiles));
+static hipError_t launch_tail(NormTailArgs c, bool rceil, bool k128, hipStream_t s) {
+  c.tiles = c.q ? (int32_t)((c.cols + kTC - 1) / kTC * ((c.rows_pad + kTR - 1) / kTR)) : 0;
+  const dim3 grid((unsigned)(c.dw_blocks + c.tiles));
   with_fmt(rceil, k128, [&](auto f) {
     hipLaunchKernelGGL((k_norm_tail<decltype(f), NORM>), grid, dim3(kFmtThreads), 0, s, c);
   });
@@ -328,10 +377,12 @@ static hipError_t launch_tail(const NormTailArgs& c, bool rceil, bool k128, hipS
 hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t s) {
   const RowShape sh = row_shape(a.cols, a.cols <= 512 ? 1 : 2);
   const dim3 grid((unsigned)((a.rows + sh.groups - 1) / sh.groups)), block(64 * sh.waves * sh.groups);
+  const NormRowPack p{a.x, a.r, a.w, a.sum, a.rstd, a.q_row, a.s_row, a.q_ck, a.s_ck, (int32_t)a.ld_x, (int32_t)a.ld_r,
+                      (int32_t)a.rows, (int32_t)a.cols, a.eps, sh.waves};
   with_fmt(a.rceil, a.k128, [&](auto f) {
     using F = decltype(f);
-    if (sh.nch == 1) hipLaunchKernelGGL((k_norm_row<F, 1>), grid, block, 0, s, a, sh.waves);
-    else hipLaunchKernelGGL((k_norm_row<F, 2>), grid, block, 0, s, a, sh.waves);
+    if (sh.nch == 1) hipLaunchKernelGGL((k_norm_row<F, 1>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((k_norm_row<F, 2>), grid, block, 0, s, p);
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.q_col) return e;
@@ -351,14 +402,17 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t s) {
   if (parts > 0) {
     const int per = (int)part_rows(a.rows, a.cols);
     const dim3 grid((unsigned)((parts + sh.groups - 1) / sh.groups)), block(64 * sh.waves * sh.groups);
+    const NormBwdPack p{a.dy, a.q_ck ? (const void*)a.q_ck : a.x, a.s_ck, a.dsum, a.w, a.rstd, a.dx, a.q_row, a.s_row,
+                        a.work, (int32_t)a.ld_dy, (int32_t)a.ld_x, (int32_t)a.ld_dsum, (int32_t)a.rows, (int32_t)a.cols,
+                        (int16_t)sh.waves, (int16_t)per};
     with_fmt(a.rceil, a.k128, [&](auto f) {
       using F = decltype(f);
       if (sh.nch == 1) {
-        if (a.q_ck) hipLaunchKernelGGL((k_norm_bwd<F, 1, true>), grid, block, 0, s, a, sh.waves, per);
-        else hipLaunchKernelGGL((k_norm_bwd<F, 1, false>), grid, block, 0, s, a, sh.waves, per);
+        if (a.q_ck) hipLaunchKernelGGL((k_norm_bwd<F, 1, true>), grid, block, 0, s, p);
+        else hipLaunchKernelGGL((k_norm_bwd<F, 1, false>), grid, block, 0, s, p);
       } else {
-        if (a.q_ck) hipLaunchKernelGGL((k_norm_bwd<F, 2, true>), grid, block, 0, s, a, sh.waves, per);
-        else hipLaunchKernelGGL((k_norm_bwd<F, 2, false>), grid, block, 0, s, a, sh.waves, per);
+        if (a.q_ck) hipLaunchKernelGGL((k_norm_bwd<F, 2, true>), grid, block, 0, s, p);
+        else hipLaunchKernelGGL((k_norm_bwd<F, 2, false>), grid, block, 0, s, p);
       }
     });
     const hipError_t e = hipGetLastError();

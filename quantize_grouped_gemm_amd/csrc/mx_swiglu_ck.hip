@@ -23,6 +23,23 @@
 
 namespace mxk {
 
+struct SwigluPack {
+  const uint16_t *a, *b;     // a: dh in the backward
+  uint8_t *q_row, *s_row, *q_col, *s_col, *q_ck, *s_ck;
+  int32_t ld, rows, hidden, bands;
+
+  template <class F>
+  __device__ SwigluCkArgs wide() const {
+    SwigluCkArgs w{};
+    w.a = a; w.b = b; w.ld_ab = ld; w.dh = a; w.ld_dh = ld;
+    w.rows = rows; w.hidden = hidden; w.rows_pad = padded<F>(rows);
+    w.q_row = q_row; w.s_row = s_row; w.q_col = q_col; w.s_col = s_col; w.q_ck = q_ck; w.s_ck = s_ck;
+    w.bands = bands;
+    return w;
+  }
+};
+static_assert(sizeof(SwigluPack) <= kArgBytes);
+
 template <class F, bool FULL>
 __device__ __forceinline__ void swiglu_ck_fwd_tile(const SwigluCkArgs& a, TileLds& l, uint32_t (&s_ck)[2][kTR], int64_t r0,
                                                    int64_t c0, int rows_valid, int rows_pad, int cols_valid) {
@@ -43,9 +60,10 @@ __device__ __forceinline__ void swiglu_ck_fwd_tile(const SwigluCkArgs& a, TileLd
 }
 
 template <class F>
-__global__ __launch_bounds__(kFmtThreads) void k_swiglu_ck_fwd(SwigluCkArgs a) {
+__global__ __launch_bounds__(kFmtThreads) void k_swiglu_ck_fwd(SwigluPack pack) {
   __shared__ TileLds l;
   __shared__ uint32_t s_ck[2][kTR];
+  const SwigluCkArgs a = pack.wide<F>();
   const TilePos at = tile_pos(blockIdx.x, (uint32_t)((a.hidden + kTC - 1) / kTC), (uint32_t)((a.rows_pad + kTR - 1) / kTR),
                               a.bands);
   const int64_t r0 = at.r0, c0 = at.c0;
@@ -122,8 +140,9 @@ __device__ __forceinline__ void swiglu_ck_bwd_tile(const SwigluCkArgs& a, TileLd
 }
 
 template <class F>
-__global__ __launch_bounds__(kFmtThreads) void k_swiglu_ck_bwd(SwigluCkArgs a) {
+__global__ __launch_bounds__(kFmtThreads) void k_swiglu_ck_bwd(SwigluPack pack) {
   __shared__ TileLds l;
+  const SwigluCkArgs a = pack.wide<F>();
   const TilePos at = tile_pos(blockIdx.x, (uint32_t)((a.hidden + kTC - 1) / kTC), (uint32_t)((a.rows_pad + kTR - 1) / kTR),
                               a.bands);
   const int64_t r0 = at.r0, c0 = at.c0;
@@ -140,27 +159,27 @@ __global__ __launch_bounds__(kFmtThreads) void k_swiglu_ck_bwd(SwigluCkArgs a) {
 // 12345 x 4096 backward 85 -> 80, 16384 x 6912 forward 193 -> 185 (8192 x 8192
 // backward 120 -> 128); with fewer rows they cost 1 to 4% (5000 x 11008
 // backward 90 against 94).
-static SwigluCkArgs with_order(SwigluCkArgs a) {
-  a.bands = a.rows_pad >= 64 * kTR;
-  return a;
+static SwigluPack pack(const SwigluCkArgs& a, const uint16_t* in, int64_t ld) {
+  return SwigluPack{in, a.b, a.q_row, a.s_row, a.q_col, a.s_col, a.q_ck, a.s_ck, (int32_t)ld, (int32_t)a.rows,
+                    (int32_t)a.hidden, a.rows_pad >= 64 * kTR};
 }
 
 static dim3 tile_grid(const SwigluCkArgs& a) {
   return dim3((unsigned)((a.hidden + kTC - 1) / kTC * ((a.rows_pad + kTR - 1) / kTR)));
 }
 
-hipError_t launch_swiglu_ck_fwd(const SwigluCkArgs& args, hipStream_t s) {
-  const SwigluCkArgs a = with_order(args);
+hipError_t launch_swiglu_ck_fwd(const SwigluCkArgs& a, hipStream_t s) {
+  const SwigluPack p = pack(a, a.a, a.ld_ab);
   with_fmt(a.rceil, a.k128, [&](auto f) {
-    hipLaunchKernelGGL(k_swiglu_ck_fwd<decltype(f)>, tile_grid(a), dim3(kFmtThreads), 0, s, a);
+    hipLaunchKernelGGL(k_swiglu_ck_fwd<decltype(f)>, tile_grid(a), dim3(kFmtThreads), 0, s, p);
   });
   return hipGetLastError();
 }
 
-hipError_t launch_swiglu_ck_bwd(const SwigluCkArgs& args, hipStream_t s) {
-  const SwigluCkArgs a = with_order(args);
+hipError_t launch_swiglu_ck_bwd(const SwigluCkArgs& a, hipStream_t s) {
+  const SwigluPack p = pack(a, a.dh, a.ld_dh);
   with_fmt(a.rceil, a.k128, [&](auto f) {
-    hipLaunchKernelGGL(k_swiglu_ck_bwd<decltype(f)>, tile_grid(a), dim3(kFmtThreads), 0, s, a);
+    hipLaunchKernelGGL(k_swiglu_ck_bwd<decltype(f)>, tile_grid(a), dim3(kFmtThreads), 0, s, p);
   });
   return hipGetLastError();
 }

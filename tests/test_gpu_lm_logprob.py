@@ -264,3 +264,27 @@ def test_fwd_around_the_launch_rules(gpu, T, V, top, dtype):
     x, t = _logits(T, V, dtype, V - T)
     print(f"T={T} V={V} top={top} {dtype}", flush=True)
     _check_fwd(lm.token_logprobs(x, t, top=top), x, t, 1.0, top)
+
+
+@pytest.mark.parametrize("T,V", [(16, 131072), (140, 70001)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fill", ["infinity", "lowest"])
+def test_fwd_allowed_sets(gpu, T, V, dtype, fill):
+    """Masks that leave 1 to 20000 tokens of a large vocabulary, scattered or next to
+    each other, in whole rows and in rows split over workgroups: alternatives
+    beyond them are the first masked tokens."""
+    top = 20
+    g = torch.Generator().manual_seed(T)
+    low = -torch.inf if fill == "infinity" else torch.finfo(dtype).min
+    counts = [1, 2, 19, 20, 21, 64, 300, 600, 1088, 1089, 5000, 20000]
+    x = torch.full((T, V), low)
+    t = torch.zeros(T, dtype=torch.int64)
+    for r in range(T):
+        n = counts[r % len(counts)]
+        at = torch.randperm(V, generator=g)[:n] if r % 2 else V // 3 + torch.arange(n)
+        x[r, at] = 2.5 * torch.randn(n, generator=g)
+        t[r] = at[0]
+    print(f"T={T} V={V} {dtype} {fill}", flush=True)
+    x = x.to(dtype).to(dev())
+    t = t.to(dev())
+    _check_fwd(lm.token_logprobs(x, t, top=top), x, t, 1.0, top)
