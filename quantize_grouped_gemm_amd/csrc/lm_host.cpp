@@ -109,8 +109,23 @@ struct Out {
     else part(s, base, at, {R, C / 32});
     return Codes{p, p + at};
   }
-  void part(PyObject* key, const Tensor& base, int64_t offset, at::IntArrayRef shape) {
-    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(), base.dtype());
+  // Small outputs of one lifetime share one allocation as well, 16-byte aligned.
+  struct Shared {
+    Tensor base;
+    int64_t at = 0;
+  };
+  Shared shared(int64_t bytes) { return Shared{Tensor(at::detail::empty_cuda({bytes}, kU8, device, std::nullopt))}; }
+  void* add(Shared& s, PyObject* key, at::IntArrayRef shape, at::ScalarType ty) {   // 4-byte types
+    void* p = static_cast<char*>(s.base.data_ptr()) + s.at;
+    int64_t n = 1;
+    for (int64_t d : shape) n *= d;
+    part(key, s.base, s.at / 4, shape, c10::scalarTypeToTypeMeta(ty));
+    s.at += up(4 * n, 16);
+    return p;
+  }
+  void part(PyObject* key, const Tensor& base, int64_t offset, at::IntArrayRef shape,
+            caffe2::TypeMeta ty = c10::scalarTypeToTypeMeta(kU8)) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(), ty);
     t.unsafeGetTensorImpl()->set_storage_offset(offset);
     t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
     PyObject* o = THPVariable_Wrap(std::move(t));
@@ -291,11 +306,12 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t top = PyLong_AsLongLongAndOverflow(a[3], &overflow);
     NOT_ORDINARY(overflow || top < 0 || top > 64 || top > l.V);
     Out out(dev);
-    float* logp = static_cast<float*>(out.add(kLogp, {l.T}, kF32));
-    float* ent = static_cast<float*>(out.add(kEntropy, {l.T}, kF32));
-    float* stats = static_cast<float*>(out.add(kStats, {l.T, 2}, kF32));
-    float* tl = top ? static_cast<float*>(out.add(kTopLogp, {l.T, top}, kF32)) : nullptr;
-    int32_t* ti = top ? static_cast<int32_t*>(out.add(kTopIdx, {l.T, top}, at::kInt)) : nullptr;
+    Out::Shared sh = out.shared(2 * up(4 * l.T, 16) + up(8 * l.T, 16) + 2 * up(4 * l.T * top, 16));
+    float* logp = static_cast<float*>(out.add(sh, kLogp, {l.T}, kF32));
+    float* ent = static_cast<float*>(out.add(sh, kEntropy, {l.T}, kF32));
+    float* stats = static_cast<float*>(out.add(sh, kStats, {l.T, 2}, kF32));
+    float* tl = top ? static_cast<float*>(out.add(sh, kTopLogp, {l.T, top}, kF32)) : nullptr;
+    int32_t* ti = top ? static_cast<int32_t*>(out.add(sh, kTopIdx, {l.T, top}, at::kInt)) : nullptr;
     const int64_t bytes = mx_token_logprobs_work(l.T, l.V, (int32_t)top);
     Tensor work;
     if (bytes) work = Tensor(at::detail::empty_cuda({bytes}, kU8, out.device, std::nullopt));

@@ -441,20 +441,21 @@ struct RowOut {
   bool empty;
 };
 
-// Target index (-1: not scored) and its logit; thread 0 only.
+// Target index (-1: not scored) and its logit, if that lies in the segment
+// [first, first + n); thread 0 only.
 struct TargetLogit {
   int64_t tg;
   float x;
 };
 
 template <bool F32>
-__device__ __forceinline__ TargetLogit target_logit(const LogprobArgs& a, int64_t row) {
+__device__ __forceinline__ TargetLogit target_logit(const LogprobArgs& a, int64_t row, int64_t first, int64_t n) {
   TargetLogit r{-1, 0.0f};
   if (threadIdx.x == 0) {
     const void* x = logits_row<F32>(a, row);
     r.tg = row_target(a, row);
-    if (a.dev_err && r.tg < 0 && a.targets[row] != a.ignore_index) atomicOr(a.dev_err, 8);
-    if (r.tg >= 0)
+    if (first == 0 && a.dev_err && r.tg < 0 && a.targets[row] != a.ignore_index) atomicOr(a.dev_err, 8);
+    if (r.tg >= first && r.tg < first + n)
       r.x = F32 ? static_cast<const float*>(x)[r.tg]
                 : __uint_as_float((uint32_t)static_cast<const uint16_t*>(x)[r.tg] << 16);
   }
@@ -476,11 +477,19 @@ __device__ __forceinline__ RowOut store_row(const LogprobArgs& a, int64_t row, S
 constexpr int kMaxParts = 16;
 constexpr int kJoinThreads = 256;
 
-// Joins the Softs of a wave's first kMaxParts lanes (every wave does the same work)
-// and stores the row.
-template <bool F32>
-__device__ __forceinline__ RowOut join_row(const LogprobArgs& a, int64_t row, Soft v, float c) {
-  const TargetLogit tl = target_logit<F32>(a, row);
+// What a segment leaves for the join: its sums and, if it holds the target, that
+// logit (the join would read it behind the target's index, one latency later).
+struct alignas(16) SegSums {
+  Soft v;
+  float xt;
+};
+
+// Joins the sums of a wave's first kMaxParts lanes, the segments of `seg` logits
+// (every wave does the same work), and stores the row.
+__device__ __forceinline__ RowOut join_row(const LogprobArgs& a, int64_t row, SegSums part, int64_t seg, float c) {
+  Soft v = part.v;
+  TargetLogit tl{row_target(a, row), 0.0f};
+  tl.x = __shfl(part.xt, tl.tg < 0 ? 0 : (int)((uint32_t)tl.tg / (uint32_t)seg));
 #pragma unroll
   for (int o = kMaxParts / 2; o >= 1; o >>= 1)
     v = soft_join(v, Soft{__shfl_xor(v.m, o), __shfl_xor(v.s, o), __shfl_xor(v.a, o)}, c);
@@ -503,20 +512,20 @@ struct Split {
   int64_t seg;
 };
 
-// Workspace of a split row: parts Softs, then (16-byte aligned) parts x top
-// keys, 0 where a segment has fewer entries.
+// Workspace of a split row: parts SegSums, then parts x top keys, 0 where a
+// segment has fewer entries.
 struct PartWork {
-  Soft* soft;
+  SegSums* soft;
   uint64_t* keys;
 };
 
 __host__ __device__ inline int64_t soft_bytes(int64_t rows, int64_t parts) {
-  return (rows * parts * (int64_t)sizeof(Soft) + 15) / 16 * 16;
+  return rows * parts * (int64_t)sizeof(SegSums);
 }
 
 __device__ __forceinline__ PartWork part_work(const LogprobArgs& a, const Split& sp) {
   char* w = static_cast<char*>(a.work);
-  return PartWork{reinterpret_cast<Soft*>(w), reinterpret_cast<uint64_t*>(w + soft_bytes(a.rows, sp.parts))};
+  return PartWork{reinterpret_cast<SegSums*>(w), reinterpret_cast<uint64_t*>(w + soft_bytes(a.rows, sp.parts))};
 }
 
 template <bool F32, bool TOP, int NT, bool STREAM>
@@ -560,8 +569,7 @@ __global__ __launch_bounds__(NT) void k_logprob_part(LogprobPack pack) {
     }
   };
   fetch(0, cur);
-  TargetLogit tl{-1, 0.0f};
-  if (sp.parts == 1) tl = target_logit<F32>(a, row);
+  const TargetLogit tl = target_logit<F32>(a, row, first, n);
   int slot = 0, left = per_slot;
   for (int tile = 0; tile < tiles; ++tile) {
     if (tile + 1 < tiles) fetch(tile + 1, nxt);
@@ -644,7 +652,7 @@ __global__ __launch_bounds__(NT) void k_logprob_part(LogprobPack pack) {
     if constexpr (TOP) store_top(a, row, l.cand, o);
   } else {
     const PartWork w = part_work(a, sp);
-    if (t == 0) w.soft[row * sp.parts + part] = v;
+    if (t == 0) w.soft[row * sp.parts + part] = SegSums{v, tl.x};
     if constexpr (TOP) {
       if (t < a.top) w.keys[(row * sp.parts + part) * a.top + t] = t < l.count ? l.cand[t] : 0;
     }
@@ -656,7 +664,7 @@ __global__ __launch_bounds__(NT) void k_logprob_part(LogprobPack pack) {
 // first entries (`lead` of each, at least `top` in all) bounds the result from
 // below; what reaches it, rarely many more than `top`, is ranked. All loads of
 // global memory are issued at the start: the kernel is a chain of latencies.
-template <bool F32, bool TOP>
+template <bool TOP>
 __global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobPack pack) {
   const LogprobArgs a = pack.wide();
   const Split sp{pack.parts, pack.seg};
@@ -664,7 +672,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobPack pack)
   const int64_t row = blockIdx.x;
   const PartWork w = part_work(a, sp);
   const float c = a.scale * kLog2e;
-  Soft v{-INFINITY, 0.0f, 0.0f};
+  SegSums v{{-INFINITY, 0.0f, 0.0f}, 0.0f};
   if (lane < sp.parts) v = w.soft[row * sp.parts + lane];
   if constexpr (TOP) {
     __shared__ uint64_t keys[kMaxParts * kMaxTop], cand[kMaxParts * kMaxTop], best[kMaxTop];
@@ -677,7 +685,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobPack pack)
       bound = 1;
       count = 0;
     }
-    const RowOut o = join_row<F32>(a, row, v, c);
+    const RowOut o = join_row(a, row, v, sp.seg, c);
     const int lead = min((2 * a.top + sp.parts - 1) / sp.parts, a.top);
     const int leads = lead * sp.parts;   // at most 2 top + parts
     __syncthreads();
@@ -701,7 +709,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobPack pack)
     __syncthreads();
     store_top(a, row, best, o);
   } else {
-    join_row<F32>(a, row, v, c);
+    join_row(a, row, v, sp.seg, c);
   }
 }
 
@@ -939,7 +947,7 @@ static hipError_t launch_fwd(const LogprobArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_logprob_part<F32, TOP, 256, false>), grid, dim3(256), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || sp.parts == 1) return e;
-  hipLaunchKernelGGL((k_logprob_join<F32, TOP>), dim3((unsigned)a.rows), dim3(kJoinThreads), 0, s, p);
+  hipLaunchKernelGGL(k_logprob_join<TOP>, dim3((unsigned)a.rows), dim3(kJoinThreads), 0, s, p);
   return hipGetLastError();
 }
 
