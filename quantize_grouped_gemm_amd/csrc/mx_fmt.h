@@ -39,18 +39,21 @@ constexpr int kFmtThreads = 512;
 constexpr int kChunks = kTR * kTC / 8 / kFmtThreads;   // 4 per thread
 constexpr int kRowStep = kFmtThreads / 16;              // rows between a thread's chunks
 
+// The id-th of n in an order where each XCD (the workgroups of equal id mod 8)
+// walks its own contiguous eighth, forwards or from its end.
+__device__ __forceinline__ uint32_t band_id(uint32_t id, uint32_t n, bool reverse) {
+  const uint32_t xcd = id & 7, i = id >> 3, len = n / 8 + (xcd < n % 8);
+  return xcd * (n / 8) + min(xcd, n % 8) + (reverse ? len - 1 - i : i);
+}
+
 struct TilePos {
   int64_t r0, c0;
 };
 
-// Tile `id` of nx x ny in row order, or, with `bands`, so that each XCD (the
-// workgroups of equal id mod 8) walks its own contiguous eighth of that order:
-// the eight then work on different rows at any time.
+// Tile `id` of nx x ny in row order, or with `bands` in bands of that order:
+// the eight XCDs then work on different rows at any time.
 __device__ __forceinline__ TilePos tile_pos(uint32_t id, uint32_t nx, uint32_t ny, bool bands) {
-  if (bands) {
-    const uint32_t n = nx * ny, xcd = id & 7;
-    id = xcd * (n / 8) + min(xcd, n % 8) + (id >> 3);
-  }
+  if (bands) id = band_id(id, nx * ny, false);
   const uint32_t y = id / nx;
   return TilePos{(int64_t)y * kTR, (int64_t)(id - y * nx) * kTC};
 }
