@@ -903,11 +903,11 @@ __global__ __launch_bounds__(kFmtThreads, F32 ? 6 : 8) void k_logprob_bwd(Logpro
 // ---------------------------------------------------------------- launch
 
 // A row is split over the vocabulary, into up to 16 segments of at least 8192
-// logits, where rows are few and long: the join costs a launch and 5 us. One
-// row of 131072 with 20 alternatives takes 11.2 us in 16 segments and 17.2
-// whole, 64 such rows 12.9 and 20.0; 200 rows take 21 either way, and rows of
-// up to 65536 are faster whole (84 x 48907 13.0 against 14.0, one row of 50000
-// 11.0 against 11.3).
+// logits, where rows are few and long: the join costs a launch and 4 us. One
+// row of 131072 with 20 alternatives takes 11.0 us in 16 segments and 15.4
+// whole, 64 such rows 14.2 and 16.6, 128 rows 17.5 and 17.1; 200 rows with 5 are
+// slower in segments (19.7 against 17.5), and so are rows of up to 65536 (84 x
+// 48907 13.9 against 12.0, one row of 50000 11.8 against 11.1).
 static Split split_rows(int64_t rows, int64_t vocab) {
   int64_t parts = 1;
   if (rows <= 128 && vocab > 65536)
