@@ -288,3 +288,19 @@ def test_fwd_allowed_sets(gpu, T, V, dtype, fill):
     x = x.to(dtype).to(dev())
     t = t.to(dev())
     _check_fwd(lm.token_logprobs(x, t, top=top), x, t, 1.0, top)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_fwd_targets_of_split_rows(gpu, dtype):
+    """Targets at the borders of a split row's segments, not scored ones, and
+    ones outside the vocabulary."""
+    V = 131072
+    at = [0, 8191, 8192, V // 2 - 1, V // 2, V - 1, -100, 7]
+    x, _ = _logits(len(at), V, dtype, 3)
+    t = torch.tensor(at).to(dev())
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    _check_fwd(lm.token_logprobs(x, t, top=3, dev_err=err), x, t, 1.0, 3)
+    assert err.item() == 0
+    t[7] = V
+    out = lm.token_logprobs(x, t, dev_err=err)
+    assert err.item() == 8 and out["logp"][7].item() == 0 and out["logp"][6].item() == 0
