@@ -356,15 +356,16 @@ __device__ __forceinline__ void offer_all(TopLds<NT>& l, const void* x, int64_t 
 
 // The `top` best entries of the segment [0, n) of x (first index idx0), in
 // descending order in l.cand[0 .. l.count). `slots` slots of `tiles` tiles
-// each; tmax the thread's maximum.
+// each; tmax the thread's maximum. Maxima leave NaN out, so a segment that has
+// one (`nan`; an infinity may count as one) is read again as a whole.
 //
 // Where most slots reach the bound, a mask (or a constant) has made it the
 // value of most entries. If equal upper halves of float32 mean equal values (bf16, and
 // -infinity in either type), the entries above it come from the few slots above it, and
 // the others are the first ones in order of their index.
 template <bool F32, int NT>
-__device__ __forceinline__ void find_top(TopLds<NT>& l, const void* x, int64_t n, uint32_t idx0, float tmax, int slots,
-                                         int tiles, int top) {
+__device__ __forceinline__ void find_top(TopLds<NT>& l, const void* x, int64_t n, uint32_t idx0, float tmax, bool nan,
+                                         int slots, int tiles, int top) {
   constexpr int kFill = 128;
   const int t = threadIdx.x;
   l.tkey[t] = (uint16_t)key16(tmax);
@@ -390,7 +391,7 @@ __device__ __forceinline__ void find_top(TopLds<NT>& l, const void* x, int64_t n
   const uint64_t thr = l.thr;
   const uint32_t bound = (uint32_t)((thr + 1) >> 48);
   bool whole = true;
-  if (2 * hits > slots * NT && (!F32 || bound == kLowest16)) {
+  if (!nan && 2 * hits > slots * NT && (!F32 || bound == kLowest16)) {
     hits = list_slots(l, slots, bound + 1);
     if (hits <= kList) {
       offer_list<F32, NT>(l, x, n, idx0, hits, tiles, thr + (1ull << 48));
@@ -408,7 +409,7 @@ __device__ __forceinline__ void find_top(TopLds<NT>& l, const void* x, int64_t n
         __syncthreads();
       }
     }
-  } else if (hits <= kList) {
+  } else if (!nan && hits <= kList) {
     offer_list<F32, NT>(l, x, n, idx0, hits, tiles, thr);
     whole = l.count > kCand;
   }
@@ -646,7 +647,7 @@ __global__ __launch_bounds__(NT) void k_logprob_part(LogprobPack pack) {
     v.a += red[2][i];
   }
 
-  if constexpr (TOP) find_top<F32, NT>(l, x, n, (uint32_t)first, tmax, slot, per_slot, a.top);
+  if constexpr (TOP) find_top<F32, NT>(l, x, n, (uint32_t)first, tmax, !(v.s == v.s), slot, per_slot, a.top);
   if (sp.parts == 1) {
     const RowOut o = store_row(a, row, v, tl);
     if constexpr (TOP) store_top(a, row, l.cand, o);
