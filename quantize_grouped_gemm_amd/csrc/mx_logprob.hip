@@ -189,8 +189,13 @@ constexpr int kSlots = 16;
 constexpr int kRound = 1024;                // entries looked at between two checks of the candidate count
 constexpr int kCand = kRound + kMaxTop;
 constexpr int kList = 512;                  // slots worth reading one by one
-constexpr float kNoRef = -1e30f;
-constexpr float kFarExp = 1e29f;            // |m c| up to here suits the fast sums
+// The fast sums hold exponents up to kFarExp in size: x c - r is rounded once,
+// but r is the rounded m c, off by up to 2^-24 |m c|, which has to stay small as
+// an exponent (at 2^32 the largest term would be 2^256). Rows whose maximum lies
+// beyond take far_sums. Entries below kNoRef never set r, so a run of them
+// (a finite mask) leaves nothing in the sums.
+constexpr float kNoRef = -0x1p28f;
+constexpr float kFarExp = 0x1p27f;
 
 template <bool F32>
 constexpr int kUnroll = F32 ? 2 : 4;

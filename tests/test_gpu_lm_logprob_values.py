@@ -51,3 +51,33 @@ def test_alternatives_of_rows_with_nan(gpu, V, dtype):
         want = min(top, int(nan[r].sum()))
         assert idx[r].unique().numel() == top, r
         assert idx[r][:want].tolist() == nan[r].nonzero().flatten()[:want].tolist(), r
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [9001, 131072])
+def test_logits_of_large_magnitude(gpu, V, dtype):
+    """Finite masks of -1e10 and -5e29 over runs of tokens and over whole rows,
+    common offsets of any size, one entry far above ordinary ones that rise from
+    tile to tile: differences of logits decide, not their size."""
+    top = 20
+    g = torch.Generator().manual_seed(V)
+    base = torch.randn(V, generator=g)
+    i = torch.arange(V)
+    run = (i >= V // 8) & (i < V - V // 4)
+
+    def masked(m, at):
+        return torch.where(at, torch.tensor(m), base)
+
+    rising = base + 22.0 * (i // 2048).float().clamp(max=3)
+    spike = rising.clone()
+    spike[V - 2] = 6e28
+    step = 2.0 ** 10 * (torch.arange(V) % 5).float()
+    rows = [masked(-1e10, run), masked(-1e10, ~run), torch.full((V,), -1e10), masked(-5e29, run), torch.full((V,), -5e29),
+            spike, rising, masked(-3e9, i != 7), masked(-1e9, run), torch.full((V,), 7e9), -1e10 + step, 2.0 ** 34 + step,
+            2.0 ** 70 * (1 + (i % 7).float()), torch.full((V,), -1.7e8) + step, base + 9e7]
+    x = torch.stack(rows).to(dtype).to(dev())
+    t = torch.full((len(rows),), 7).to(dev())
+    t[1::2] = V - 3
+    print(f"V={V} {dtype}", flush=True)
+    _check_fwd(lm.token_logprobs(x, t, scale=0.7, top=top), x, t, float(torch.tensor(0.7)), top)
+    _check_fwd(lm.token_logprobs(x, t, top=top), x, t, 1.0, top)
