@@ -422,6 +422,15 @@ __device__ __forceinline__ void find_top(TopLds<NT>& l, const void* x, int64_t n
   keep_top(l, top);
 }
 
+// A of sums s whose exponents all gain d. The product is rounded by itself (no
+// fused product-sum): where s is one term 2^-d, A is its product with -d, rounded,
+// and both cancel to exactly 0, the entropy of a row with one token left.
+__device__ __forceinline__ float shift_a(float A, float s, float d) {
+#pragma clang fp contract(off)
+  const float sd = s * d;
+  return A + sd;
+}
+
 // S and A of the segment relative to its maximum m, by the definition; for
 // maxima whose exponents the fast sums cannot hold.
 template <bool F32, int NT>
@@ -468,12 +477,15 @@ __device__ __forceinline__ TargetLogit target_logit(const LogprobArgs& a, int64_
   return r;
 }
 
+// S >= 1 (it holds the maximum's own term 1) and A <= 0 but for rounding, which
+// is kept from the entropy (by a comparison that leaves NaN alone).
 __device__ __forceinline__ RowOut store_row(const LogprobArgs& a, int64_t row, Soft v, TargetLogit tl) {
   const bool empty = v.m == -INFINITY && v.s == 0.0f;
   const float ls = empty ? -INFINITY : logf(v.s);
+  const float ent = ls - kLn2 * (v.a / v.s);
   if (threadIdx.x == 0) {
     a.logp[row] = tl.tg < 0 ? 0.0f : empty ? -INFINITY : (tl.x - v.m) * a.scale - ls;
-    a.entropy[row] = empty ? 0.0f : ls - kLn2 * (v.a / v.s);
+    a.entropy[row] = empty || ent < 0.0f ? 0.0f : ent;
     a.stats_out[2 * row] = v.m;
     a.stats_out[2 * row + 1] = ls;
   }
@@ -591,7 +603,7 @@ __global__ __launch_bounds__(NT) void k_logprob_part(LogprobPack pack) {
       const float r = __builtin_rintf(m * c);
       const float d = ref - r;
       const float g = __builtin_amdgcn_exp2f(d);
-      A = (A + s * d) * g;
+      A = shift_a(A, s, d) * g;
       s *= g;
       ref = r;
     }
@@ -628,11 +640,15 @@ __global__ __launch_bounds__(NT) void k_logprob_part(LogprobPack pack) {
   if (M != -INFINITY && !(fabsf(M) * c <= kFarExp)) {
     v = far_sums<F32, NT>(x, n, M, c);
   } else {
-    // relative to M itself: r - M c, then the factor 2^(r - M c)
+    // relative to M itself: divided by M's own term, which the sums hold with
+    // these very bits. So S is never below 1, and exactly 1 (A exactly 0) where one
+    // token is left; a factor 2^(r - M c) would be a second rounded exponential, with
+    // log probabilities an ulp above 0. (Infinite where all of a thread's terms
+    // are 0.)
     const float base = M == -INFINITY ? 0.0f : M;
-    const float d = fmaf(-base, c, ref);
-    const float g = __builtin_amdgcn_exp2f(d);
-    v = Soft{M, s * g, (A + s * d) * g};
+    const float d = fmaf(base, c, -ref);
+    const float e = __builtin_amdgcn_exp2f(d);
+    v = Soft{M, s / e, shift_a(A, s, -d) / e};
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {

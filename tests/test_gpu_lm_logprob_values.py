@@ -81,3 +81,29 @@ def test_logits_of_large_magnitude(gpu, V, dtype):
     print(f"V={V} {dtype}", flush=True)
     _check_fwd(lm.token_logprobs(x, t, scale=0.7, top=top), x, t, float(torch.tensor(0.7)), top)
     _check_fwd(lm.token_logprobs(x, t, top=top), x, t, 1.0, top)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [700, 9001, 100003])
+def test_rows_with_one_token_left(gpu, V, dtype):
+    """The only token left has probability 1: log probability and entropy are
+    exactly 0, wherever it stands and whatever its logit is; next to tokens that
+    are all but impossible, no log probability is above 0 and no entropy below."""
+    T = 300
+    g = torch.Generator().manual_seed(V)
+    x = torch.full((T, V), -INF)
+    t = torch.randint(0, V, (T,), generator=g)
+    x[torch.arange(T), t] = 12.0 * torch.randn(T, generator=g)
+    for rows in (T, 100):                     # 100: rows that long are split over workgroups
+        for scale in (1.0, 0.83):
+            xd, td = x[:rows].to(dtype).to(dev()), t[:rows].to(dev())
+            out = lm.token_logprobs(xd, td, scale=scale, top=2)
+            for k in ("logp", "entropy"):
+                assert not out[k].any(), (k, int((out[k] != 0).sum()))
+            assert not out["stats"][:, 1].any() and not out["top_logp"][:, 0].any()
+            # others from 15 to 40 below
+            near = torch.where(x[:rows] == -INF, 15.0 + 25.0 * torch.rand((rows, V), generator=g), 0.0)
+            near = (x[:rows].amax(-1, keepdim=True) - near / scale).to(dtype).to(dev())
+            out = lm.token_logprobs(near, td, scale=scale, top=2)
+            assert (out["logp"] <= 0).all() and (out["entropy"] >= 0).all() and (out["stats"][:, 1] >= 0).all()
+            assert (out["top_logp"] <= 0).all()
