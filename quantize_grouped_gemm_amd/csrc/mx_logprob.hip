@@ -763,26 +763,75 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobPack pack)
 // them every constant.) l_j is formed from x c as well, so rows whose m c is
 // large (at the extreme, all entries at the lowest finite value) take their
 // differences from m first: base = m, else 0.
-struct GradRow {
+struct RowLine {
   float low;         // bound of x - base
   float mk;          // 1.5 * 2^23 + 64 - ki
   float k1, k0;      // gradient = 2^f 2^(n + 64) (k1 (x - base) + k0)
   int32_t target;    // column within the tile, out of [0, 128) if elsewhere
-  float add;         // scale dlogp, at the target
   float base;
 };
+struct GradRow : RowLine {
+  float at;          // the gradient at the target, formed by other waves than the rest
+};
+
+// The gradient at the target itself,
+//   scale dlogp (1 - p) - scale dent p (l + entropy),
+// cancels where p is near 1, as well-predicted targets have it: 1 - p taken from
+// the p above would keep few digits of it (an error of 1 to 5% at 1 - p = 6e-6). So
+// it is formed once a row, from l = (x - m) scale - ls, whose two parts have one
+// sign and which is as exact as they are, and 1 - e^l. dlogp, dent: times scale.
+__device__ __forceinline__ float target_value(float x, float m, float ls, float scale, float dlogp, float dent,
+                                              float entropy) {
+  float l = fmaf(x - m, scale, -ls);
+  l = l < -1e4f ? -1e4f : l;               // keeps NaN; e^l is 0 from -104 on
+  // 1 - e^l: above -ln 2 by its power series (what follows l^9 / 9! is below 2^-26
+  // of it), below by e^l <= 1/2, which costs no digits
+  float q = 1.0f / 362880;
+  q = fmaf(q, l, 1.0f / 40320);
+  q = fmaf(q, l, 1.0f / 5040);
+  q = fmaf(q, l, 1.0f / 720);
+  q = fmaf(q, l, 1.0f / 120);
+  q = fmaf(q, l, 1.0f / 24);
+  q = fmaf(q, l, 1.0f / 6);
+  q = fmaf(q, l, 0.5f);
+  q = -l * fmaf(q, l, 1.0f);
+  const float e = exp_nonpos(l);
+  const bool near = l > -0.6931f;
+  const float p = near ? 1.0f - q : e;
+  q = near ? q : 1.0f - e;
+  return fmaf(dlogp, q, -dent * (p * (l + entropy)));
+}
 
 constexpr float kMagic = 12582912.0f;      // 1.5 * 2^23
 constexpr float kFarRow = 1024.0f;         // |m c| from which base = m
 constexpr double kAt = -16.0;              // log2 p where c's rounding is made up for
 
 template <bool FAR>
-__device__ __forceinline__ float grad_value(float x, const GradRow& g, float c, float add) {
+__device__ __forceinline__ float grad_value(float x, const GradRow& g, float c) {
   const float y = fmaxf(FAR ? x - g.base : x, g.low);
   const float w = fmaf(y, c, g.mk);
   const float f = fmaf(y, c, g.mk - w);    // mk - w = -(ki + n), exactly
   const uint32_t p = __float_as_uint(__builtin_amdgcn_exp2f(f)) + (__float_as_uint(w) << 23);
-  return fmaf(__uint_as_float(p), fmaf(y, g.k1, g.k0), add);
+  return fmaf(__uint_as_float(p), fmaf(y, g.k1, g.k0), 0.0f);
+}
+
+// What a row's gradient is formed from. A missing operand's load is issued as
+// well (of an entropy), which keeps all of them in flight together: behind
+// branches they wait for each other, 57.6 us in place of 53.3 at 1024 x 50304
+// float32.
+struct RowIn {
+  int64_t target;                      // -1: not scored
+  bool outside;                        // not in the vocabulary
+  float m, ls, dlogp, dent, entropy;   // dlogp 0 if not scored, entropy 0 without dent
+};
+
+__device__ __forceinline__ RowIn row_in(const LogprobArgs& a, int64_t row) {
+  const int64_t t = a.targets[row];
+  const float2 stats = reinterpret_cast<const float2*>(a.stats)[row];
+  const float d = (a.dlogp ? a.dlogp : a.ent_in)[row], e = (a.dent ? a.dent : a.ent_in)[row], h = a.ent_in[row];
+  const bool in = t >= 0 && t < a.vocab, scored = in && t != a.ignore_index;
+  return RowIn{scored ? t : -1, !in && t != a.ignore_index, stats.x, stats.y, scored && a.dlogp ? d : 0.0f,
+               a.dent ? e : 0.0f, a.dent ? h : 0.0f};
 }
 
 template <bool F32, bool FAR>
@@ -798,14 +847,15 @@ __device__ __forceinline__ uint4 grad_chunk(RawChunk<F32> raw, const GradRow& ro
   if constexpr (F32) __builtin_memcpy(f, &raw, 32);
   else unpack8(raw.w[0], f);
   const uint32_t hit = (uint32_t)g.target - col;
-  if (hit < 8) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = grad_value<FAR>(f[k], g, c, (int)hit == k ? g.add : 0.0f);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = grad_value<FAR>(f[k], g, c, 0.0f);
-  }
+  for (int k = 0; k < 8; ++k) f[k] = grad_value<FAR>(f[k], g, c);
   uint4 v = pack8(f);
+  if (hit < 8) {
+    const uint32_t t = pack_bf16x2(g.at, g.at), sel = hit & 1 ? 0x05040100u : 0x03020504u;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = (int)(hit >> 1) == k ? __builtin_amdgcn_perm(t, w[k], sel) : w[k];
+  }
   asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
   return v;
 }
@@ -845,35 +895,42 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
   }
   bool row_far = false;
   if ((int)t < kTR) {
-    GradRow g{};
+    RowLine g{};
     g.mk = kMagic + 64.0f;
     g.target = -1;
     if (FULL || (int)t < rows_valid) {
-      const int64_t row = r0 + t;
-      const float m = a.stats[2 * row], ls = a.stats[2 * row + 1];
-      const int64_t tg = row_target(a, row);
-      if (c0 == 0 && a.dev_err && tg < 0 && a.targets[row] != a.ignore_index) atomicOr(a.dev_err, 8);
+      const RowIn in = row_in(a, r0 + t);
+      const float m = in.m, ls = in.ls;
+      if (c0 == 0 && a.dev_err && in.outside) atomicOr(a.dev_err, 8);
       if (!(m == -INFINITY && ls == -INFINITY)) {   // a row with nothing left has gradient 0
         row_far = !(fabsf(m) * c <= kFarRow);
-        const float d = tg >= 0 && a.dlogp ? a.dlogp[row] : 0.0f;
-        const float dent = a.dent ? a.dent[row] : 0.0f;
-        double K = fma(row_far ? 0.0 : (double)m, cd, (double)ls * kLog2eD);
-        K -= (K + kAt) * ((cd - (double)c) / cd);
-        const double ki = rint(K), kf = K - ki;
-        const float fold = __builtin_amdgcn_exp2f((float)-kf) * 0x1p-64f;
-        const double k1 = -(double)a.scale * a.scale * dent;   // times y: scale dent l_j up to a constant
+        // first what does not need K (the registers for all of it at once would
+        // spill, with the tile's logits in flight)
         const double l0 = -((double)ls + (row_far ? 0.0 : (double)m * a.scale));   // l_j at y = 0
-        const double k0 = -(double)a.scale * (a.dent ? fma((double)dent, (double)a.ent_in[row] + l0, (double)d) : (double)d);
-        g.low = ((float)ki - 186.0f) / c;
+        g.k1 = -a.scale * (a.scale * in.dent);   // times y: scale dent l_j up to a constant
+        g.k0 = (float)(-(double)a.scale * fma((double)in.dent, (double)in.entropy + l0, (double)in.dlogp));
+        asm volatile("" : "+v"(g.k1), "+v"(g.k0));
+        const float rc = __builtin_amdgcn_rcpf(c);
+        double K = fma(row_far ? 0.0 : (double)m, cd, (double)ls * kLog2eD);
+        K -= (K + kAt) * (double)((float)(cd - (double)c) * rc);
+        const double ki = rint(K);
+        const float fold = __builtin_amdgcn_exp2f((float)(ki - K)) * 0x1p-64f;
+        g.low = ((float)ki - 186.0f) * rc;
         g.mk = kMagic + 64.0f - (float)ki;
-        g.k1 = (float)k1 * fold;
-        g.k0 = (float)k0 * fold;
+        g.k1 *= fold;
+        g.k0 *= fold;
         g.base = row_far ? m : 0.0f;
-        g.add = a.scale * d;
-        g.target = tg >= c0 && tg < c0 + kTC ? (int32_t)(tg - c0) : -1;
+        g.target = in.target >= c0 && in.target < c0 + kTC ? (int32_t)(in.target - c0) : -1;
       }
     }
-    rows[t] = g;
+    static_cast<RowLine&>(rows[t]) = g;
+  } else if ((int)t < 2 * kTR && (FULL || (int)t - kTR < rows_valid)) {   // waves without a row: the targets' own values
+    const RowIn in = row_in(a, r0 + t - kTR);
+    if (in.target >= c0 && in.target < c0 + kTC) {
+      float x[1];
+      load_logits<F32>(logits_row<F32>(a, r0 + t - kTR), in.target, a.vocab, 0.0f, x);
+      rows[t - kTR].at = target_value(x[0], in.m, in.ls, a.scale, a.scale * in.dlogp, a.scale * in.dent, in.entropy);
+    }
   }
   if ((int)t < kTR) {
     const bool any = __any(row_far);
