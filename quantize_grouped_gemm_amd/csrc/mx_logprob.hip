@@ -762,7 +762,10 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobPack pack)
 // 2^-64. (A NaN among the logits has made the row's statistics NaN, and with
 // them every constant.) l_j is formed from x c as well, so rows whose m c is
 // large (at the extreme, all entries at the lowest finite value) take their
-// differences from m first: base = m, else 0.
+// differences from m first: base = m, else 0. So do rows in which the two parts of
+// k1 x + k0 are far larger than what they leave at x = m: those that only the
+// entropy reaches and where one token holds nearly all of the probability, with
+// l + entropy a few times 1e-4 there.
 struct RowLine {
   float low;         // bound of x - base
   float mk;          // 1.5 * 2^23 + 64 - ki
@@ -803,7 +806,8 @@ __device__ __forceinline__ float target_value(float x, float m, float ls, float 
 }
 
 constexpr float kMagic = 12582912.0f;      // 1.5 * 2^23
-constexpr float kFarRow = 1024.0f;         // |m c| from which base = m
+constexpr float kFarRow = 1024.0f;         // |m c| from which base = m,
+constexpr float kFarSum = 256.0f;          // and |k1 m| in its sum with k0: 2^-24 |k0| is then 2^-16 of the sum
 constexpr double kAt = -16.0;              // log2 p where c's rounding is made up for
 
 template <bool FAR>
@@ -903,12 +907,12 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
       const float m = in.m, ls = in.ls;
       if (c0 == 0 && a.dev_err && in.outside) atomicOr(a.dev_err, 8);
       if (!(m == -INFINITY && ls == -INFINITY)) {   // a row with nothing left has gradient 0
-        row_far = !(fabsf(m) * c <= kFarRow);
         // first what does not need K (the registers for all of it at once would
-        // spill, with the tile's logits in flight)
-        const double l0 = -((double)ls + (row_far ? 0.0 : (double)m * a.scale));   // l_j at y = 0
-        g.k1 = -a.scale * (a.scale * in.dent);   // times y: scale dent l_j up to a constant
-        g.k0 = (float)(-(double)a.scale * fma((double)in.dent, (double)in.entropy + l0, (double)in.dlogp));
+        // spill, with the tile's logits in flight): k1, and the value at x = m
+        g.k1 = -a.scale * (a.scale * in.dent);
+        const float at_m = -a.scale * fmaf(in.dent, in.entropy - ls, in.dlogp);
+        row_far = !(fabsf(m) * c <= kFarRow && fabsf(g.k1 * m) <= kFarSum * fabsf(at_m));
+        g.k0 = (float)fma(-(double)g.k1, row_far ? 0.0 : (double)m, (double)at_m);
         asm volatile("" : "+v"(g.k1), "+v"(g.k0));
         const float rc = __builtin_amdgcn_rcpf(c);
         double K = fma(row_far ? 0.0 : (double)m, cd, (double)ls * kLog2eD);
