@@ -132,7 +132,8 @@ mx_status mx_token_logprobs(const void* x, mx_dtype x_dtype, int64_t ld,
  * is filled up with zeros to V_pad, the next multiple of the layout's step:
  * q_row [rows, V_pad], s_row MX(G) along the vocabulary; q_col
  * [V_pad, T_pad], s_col along the rows. A row with nothing left has gradient
- * 0. ld <= 2^26 and vocab <= 2^26 - 128 for bf16, half of that for float32. */
+ * 0, and so has an entry that is ruled out, unless it is the target, as long as
+ * scale * |dlogp| and 1024 * scale * |dent| stay below 2^100. ld <= 2^26 and vocab <= 2^26 - 128 for bf16, half of that for float32. */
 mx_status mx_token_logprobs_bwd(const void* x, mx_dtype x_dtype, int64_t ld,
                                 int64_t rows, int64_t vocab,
                                 const int64_t* targets, int64_t ignore_index,

@@ -756,20 +756,22 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobPack pack)
 // by 2^n as instructions of their own, take 4096 x 131072 from 429 to 407 us
 // (5.4 TB/s) and 6000 x 100001 from 588 to 565.
 //
-// x is bounded below where x c - ki is -186: a masked entry then gives 2^-186
-// times a finite number, 0 in bf16 for every gradient below 2^52. The exponent
-// field holds n + 64, which keeps it positive, and the constants the factor
-// 2^-64. (A NaN among the logits has made the row's statistics NaN, and with
-// them every constant.) l_j is formed from x c as well, so rows whose m c is
-// large (at the extreme, all entries at the lowest finite value) take their
-// differences from m first: base = m, else 0. So do rows in which the two parts of
-// k1 x + k0 are far larger than what they leave at x = m: those that only the
-// entropy reaches and where one token holds nearly all of the probability, with
-// l + entropy a few times 1e-4 there.
+// The exponent field holds n + up, and the constants the factor 2^-up; x is
+// bounded below where n + up is -122, so that a masked entry stays a number. up
+// follows the size of the row's gradient, 2^(up - 60): the constants are then about
+// 2^-60, far from float32's ends, and a masked entry gives 2^-180, 0 in bf16 (up is
+// at most 124, for fields up to 252: exact zeros up to 2^100). A NaN among the logits
+// has made the row's statistics NaN, and with them every constant.
+//
+// l_j is formed from x c as well, so rows whose m c is large (at the extreme, all
+// entries at the lowest finite value) take their differences from m first: base =
+// m, else 0. So do rows in which the two parts of k1 x + k0 are far larger than what
+// they leave at x = m: those that only the entropy reaches and where one token holds
+// nearly all of the probability, with l + entropy a few times 1e-4 there.
 struct RowLine {
   float low;         // bound of x - base
-  float mk;          // 1.5 * 2^23 + 64 - ki
-  float k1, k0;      // gradient = 2^f 2^(n + 64) (k1 (x - base) + k0)
+  float mk;          // 1.5 * 2^23 + up - ki
+  float k1, k0;      // gradient = 2^f 2^(n + up) (k1 (x - base) + k0)
   int32_t target;    // column within the tile, out of [0, 128) if elsewhere
   float base;
 };
@@ -809,6 +811,11 @@ constexpr float kMagic = 12582912.0f;      // 1.5 * 2^23
 constexpr float kFarRow = 1024.0f;         // |m c| from which base = m,
 constexpr float kFarSum = 256.0f;          // and |k1 m| in its sum with k0: 2^-24 |k0| is then 2^-16 of the sum
 constexpr double kAt = -16.0;              // log2 p where c's rounding is made up for
+
+// up for a gradient of this size (any bits: infinity and NaN count as 2^128).
+__device__ __forceinline__ int grad_up(float size) {
+  return min((int)((__float_as_uint(size) >> 23) & 255) - 127 + 60, 124);
+}
 
 template <bool FAR>
 __device__ __forceinline__ float grad_value(float x, const GradRow& g, float c) {
@@ -900,7 +907,7 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
   bool row_far = false;
   if ((int)t < kTR) {
     RowLine g{};
-    g.mk = kMagic + 64.0f;
+    g.mk = kMagic;
     g.target = -1;
     if (FULL || (int)t < rows_valid) {
       const RowIn in = row_in(a, r0 + t);
@@ -909,8 +916,10 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
       if (!(m == -INFINITY && ls == -INFINITY)) {   // a row with nothing left has gradient 0
         // first what does not need K (the registers for all of it at once would
         // spill, with the tile's logits in flight): k1, and the value at x = m
-        g.k1 = -a.scale * (a.scale * in.dent);
-        const float at_m = -a.scale * fmaf(in.dent, in.entropy - ls, in.dlogp);
+        const int up = grad_up(a.scale * (fabsf(in.dlogp) + 1024.0f * fabsf(in.dent)));   // |l + entropy| reaches some 1000
+        const float unit = ldexpf(1.0f, -up), dent = in.dent * unit;
+        g.k1 = -a.scale * (a.scale * dent);
+        const float at_m = -a.scale * fmaf(dent, in.entropy - ls, in.dlogp * unit);
         row_far = !(fabsf(m) * c <= kFarRow && fabsf(g.k1 * m) <= kFarSum * fabsf(at_m));
         g.k0 = (float)fma(-(double)g.k1, row_far ? 0.0 : (double)m, (double)at_m);
         asm volatile("" : "+v"(g.k1), "+v"(g.k0));
@@ -918,9 +927,9 @@ __device__ __forceinline__ void logprob_bwd_tile(const LogprobArgs& a, TileLds& 
         double K = fma(row_far ? 0.0 : (double)m, cd, (double)ls * kLog2eD);
         K -= (K + kAt) * (double)((float)(cd - (double)c) * rc);
         const double ki = rint(K);
-        const float fold = __builtin_amdgcn_exp2f((float)(ki - K)) * 0x1p-64f;
-        g.low = ((float)ki - 186.0f) * rc;
-        g.mk = kMagic + 64.0f - (float)ki;
+        const float fold = __builtin_amdgcn_exp2f((float)(ki - K));
+        g.low = ((float)ki - (float)(up + 122)) * rc;
+        g.mk = kMagic + (float)up - (float)ki;
         g.k1 *= fold;
         g.k0 *= fold;
         g.base = row_far ? m : 0.0f;

@@ -181,3 +181,39 @@ def test_entropy_gradient_of_sure_rows(gpu, dtype, offset):
     at = other[torch.arange(T), x.argmax(-1).cpu()]
     print(f"{dtype} offset={offset}: {int(at.sum())} of {T} best tokens, {int(other.sum())} of all", flush=True)
     assert int(at.sum()) <= 3
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("which", ["dlogp", "dent", "both"])
+def test_gradients_of_any_size(gpu, dtype, which):
+    """Incoming gradients from 1e-28 to 1e30 (in turn by row) keep their digits,
+    masked tokens stay exactly 0, and rows next to each other do not meet."""
+    T, V = 130, 1000
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn((T, V), generator=g) * 2.5
+    t = torch.randint(0, V, (T,), generator=g)
+    x[:, V // 3:V // 2] = -INF
+    x[torch.arange(T), t] = 3.0
+    x, t = x.to(dtype).to(dev()), t.to(dev())
+    f = lm.token_logprobs(x, t)
+    size = 10.0 ** (-28 + 58 * (torch.randperm(T, generator=g).to(F64) / (T - 1)))
+    dlogp, dent = ((size * (1 + torch.rand(T, generator=g))).float() for _ in range(2))
+    if which == "dlogp":
+        dent = torch.zeros(T)
+    if which == "dent":
+        dlogp = torch.zeros(T)
+    out = lm.token_logprobs_bwd(x, t, f["stats"], f["entropy"], dlogp.to(dev()), dent.to(dev()), layout="plain")
+    x64, tc = x.cpu().to(F64), t.cpu()
+    m, ls = f["stats"].cpu().to(F64).unbind(1)
+    ent = f["entropy"].cpu().to(F64)
+    grad = _gradient(x, t, f, dlogp, dent, 1.0)
+    lp = torch.where(x64 == -INF, 0.0, x64 - m[:, None] - ls[:, None])
+    p = torch.where(x64 == -INF, 0.0, lp.exp())
+    mag = p * (dlogp.abs()[:, None] + dent.abs()[:, None] * (lp.abs() + ent.abs()[:, None]))
+    mag[torch.arange(T), tc] += dlogp.abs()
+    Vp = lm.padded_rows(V, "plain")
+    pad = lambda v: torch.cat([v, v.new_zeros(T, Vp - V)], 1)
+    R.check_codes(out["q_row"], out["s_row"], pad(grad), "rceil", which, pad(mag))
+    gone = torch.nn.functional.pad(x == -INF, (0, Vp - V), value=True)
+    gone[torch.arange(T), t] = False
+    assert not (out["q_row"] & 0x7F)[gone].any()
