@@ -47,10 +47,11 @@ bool whole(const Tensor* t, at::ScalarType ty, std::initializer_list<int64_t> sh
   return t && t->scalar_type() == ty && t->sizes() == at::IntArrayRef(shape) && t->is_contiguous();
 }
 
-// Row stride of a matrix of contiguous rows, or -1.
+// Row stride of a matrix of contiguous rows, or -1. Strides that no second row
+// or column makes use of do not matter.
 int64_t rows_ld(const Tensor* t, at::ScalarType ty, int64_t R, int64_t C) {
-  if (!t || t->scalar_type() != ty || t->dim() != 2 || t->size(0) != R || t->size(1) != C || t->stride(1) != 1 ||
-      t->stride(0) < C)
+  if (!t || t->scalar_type() != ty || t->dim() != 2 || t->size(0) != R || t->size(1) != C ||
+      (C > 1 && t->stride(1) != 1) || (R > 1 && t->stride(0) < C))
     return -1;
   return R > 1 ? t->stride(0) : C;
 }

@@ -111,14 +111,15 @@ def _matrix(t, name, dtypes=(_BF,)):
 
 
 def _rows(t, name, dtype, shape):
-    """Checks a matrix of contiguous rows; returns its row stride (that of a
-    single row does not matter)."""
+    """Checks a matrix of contiguous rows; returns its row stride (strides that
+    no second row or column makes use of do not matter)."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
         _want_rows(t, name, dtype, shape)
+    R, C = shape
     ld, one = t.stride()
-    if one != 1 or ld < shape[1]:
+    if (C > 1 and one != 1) or (R > 1 and ld < C):
         _want_rows(t, name, dtype, shape)
-    return ld if shape[0] > 1 else shape[1]
+    return ld if R > 1 else C
 
 
 def _whole(t, name, dtype, shape):
