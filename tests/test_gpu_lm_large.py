@@ -1,0 +1,123 @@
+"""The variants of the layer-boundary operators that large calls take: groups of
+several rows in the norm's backward, tiles and rows in plain order, logits and
+codes that go past the caches. Where rows do not depend on each other, results are
+compared bit for bit with calls over slices of rows, which stay below those limits
+(the other test files check them against the 64-bit formulas)."""
+
+import pytest
+import torch
+
+import lm_ref as R
+from _helpers import dev
+from quantize_grouped_gemm_amd import lm, synth
+from test_gpu_lm_norm import _eq, _mx_cols, _mx_rows, _rows
+
+pytestmark = pytest.mark.gpu
+F64, BF, F32 = torch.float64, torch.bfloat16, torch.float32
+
+# T, C, layout; rows of a group in the backward. Below and above 8M elements, one
+# and two chunks a thread, one and several rows at a time in a workgroup, last
+# groups that are not full
+NORM = [(1001, 7168, "k128"), (9001, 1024, "k128"), (601, 16384, "k128"), (2101, 4128, "plain"), (8203, 480, "plain")]
+
+
+@pytest.mark.parametrize("T,C,layout", NORM)
+def test_norm_fwd(gpu, T, C, layout):
+    print(f"T={T} C={C} {layout}", flush=True)
+    g = synth.generator(T + C)
+    x, _ = _rows(T, C, 1.0, g, pad=8)
+    r, _ = _rows(T, C, 0.5, g)
+    w = (1 + 0.1 * torch.randn(C, generator=g)).to(dev())
+    out = lm.add_rmsnorm_quant(x, w, r, layout=layout, colwise=True, checkpoint=True)
+    for i in range(0, T, 256):
+        rows = slice(i, min(i + 256, T))
+        part = lm.add_rmsnorm_quant(x[rows], w, r[rows], layout=layout, checkpoint=True)
+        for k in ("sum", "rstd", "q_row", "q_ck"):
+            _eq(out[k][rows], part[k], (k, i))
+        for k in ("s_row", "s_ck"):
+            _eq(out[k][:, rows] if layout == "k128" else out[k][rows], part[k], (k, i))
+    # y as the kernel forms it (see test_norm_fwd of the smaller shapes)
+    s, rstd = out["sum"].float(), out["rstd"][:, None]
+    h = (rstd.view(torch.int32) & -65536).view(F32)
+    y = ((s * h).to(F64) * w.to(F64) + ((s * (rstd - h)) * w).to(F64)).float().to(BF)
+    ref = _mx_cols(y, "rceil", layout)
+    _eq(out["q_col"], ref["q_col"], "q_col")
+    _eq(out["s_col"], ref["s_col"], "s_col")
+
+
+@pytest.mark.parametrize("ckpt", [False, True])
+@pytest.mark.parametrize("T,C,layout", NORM)
+def test_norm_bwd(gpu, T, C, layout, ckpt):
+    print(f"T={T} C={C} {layout} ckpt={ckpt}", flush=True)
+    g = synth.generator(T * 3 + C)
+    x, _ = _rows(T, C, 1.0, g, pad=8)
+    dy, dy64 = _rows(T, C, 1e-2, g)
+    ds, _ = _rows(T, C, 1e-2, g, pad=16)
+    w = (1 + 0.1 * torch.randn(C, generator=g)).to(dev())
+    f = lm.add_rmsnorm_quant(x, w, layout=layout, checkpoint=True)
+
+    def call(rows, whole):
+        src = dict(x=x[rows])
+        if ckpt:
+            s = f["s_ck"][:, rows] if layout == "k128" else f["s_ck"][rows]
+            src = dict(checkpoint=(f["q_ck"][rows], s.contiguous()))
+        return lm.add_rmsnorm_bwd(dy[rows], w, f["rstd"][rows], dsum=ds[rows], layout=layout, colwise=whole, **src)
+
+    out, again = call(slice(0, T), True), call(slice(0, T), True)
+    for k in out:
+        _eq(out[k], again[k], k)
+    for i in range(0, T, 128):       # one row a group
+        rows = slice(i, min(i + 128, T))
+        _eq(out["dx"][rows], call(rows, False)["dx"], ("dx", i))
+    ref = _mx_rows(out["dx"], "rceil", layout)
+    _eq(out["q_row"], ref["q_row"], "q_row")
+    _eq(out["s_row"], ref["s_row"], "s_row")
+    ref = _mx_cols(out["dx"], "rceil", layout)
+    _eq(out["q_col"], ref["q_col"], "q_col")
+    _eq(out["s_col"], ref["s_col"], "s_col")
+    # dw: up to 16 rows in turn, then a thread's parts (at most 4096 / 256 in each of 4 sums), 2 joins of
+    # those and 64 threads in turn: at most 98 roundings of the sum of magnitudes
+    s64 = x.cpu().to(F64)
+    if ckpt:
+        s64 = torch.from_numpy(R.O.dequantize(f["q_ck"].cpu().numpy(), R.plain_scales(f["s_ck"])))
+    t = dy64 * (s64 * f["rstd"].cpu().to(F64)[:, None])
+    assert torch.all((out["dw"].cpu().to(F64) - t.sum(0)).abs() <= 100 * 2.0 ** -24 * t.abs().sum(0))
+
+
+# above 2^28 codes: aligned rows, the same in bands of tiles, rows that start at odd elements
+GRAD = [(2200, 131072, BF), (2200, 131072, F32), (4224, 65536, BF), (2700, 100001, BF), (2700, 100001, F32)]
+
+
+@pytest.mark.parametrize("T,V,dtype", GRAD)
+def test_loss_gradient(gpu, T, V, dtype):
+    print(f"T={T} V={V} {dtype}", flush=True)
+    g = torch.Generator(device=dev()).manual_seed(V)
+    x = (torch.randn((T, V), generator=g, device=dev()) * 2.5).to(dtype)
+    t = torch.randint(0, V, (T,), generator=g, device=dev())
+    f = lm.token_logprobs(x, t)
+    dl, de = torch.randn(T, generator=g, device=dev()) / T, torch.randn(T, generator=g, device=dev()) / T
+    out = lm.token_logprobs_bwd(x, t, f["stats"], f["entropy"], dl, de)
+    for r0 in range(0, T, 1024):
+        r = slice(r0, min(r0 + 1024, T))
+        part = lm.token_logprobs_bwd(x[r], t[r], f["stats"][r], f["entropy"][r], dl[r], de[r])
+        n = part["q_col"].shape[1]
+        assert torch.equal(out["q_row"][r], part["q_row"]) and torch.equal(out["s_row"][:, r], part["s_row"])
+        assert torch.equal(out["q_col"][:, r0:r0 + n], part["q_col"])
+        assert torch.equal(out["s_col"][r0 // 128:(r0 + n) // 128], part["s_col"])
+
+
+@pytest.mark.parametrize("T,V,dtype", [(1100, 131072, BF), (600, 131072, F32), (2700, 50001, BF), (1400, 50001, F32)])
+@pytest.mark.parametrize("top", [0, 20])
+def test_scoring(gpu, T, V, dtype, top):
+    """More than 256 MB of logits."""
+    print(f"T={T} V={V} {dtype} top={top}", flush=True)
+    g = torch.Generator(device=dev()).manual_seed(V + T)
+    x = (torch.randn((T, V), generator=g, device=dev()) * 2.5).to(dtype)
+    t = torch.randint(0, V, (T,), generator=g, device=dev())
+    t[::7] = -100
+    out = lm.token_logprobs(x, t, scale=0.9, top=top)
+    n = (T + 1) // 2                 # above 256 rows: the same workgroups
+    for r in (slice(0, n), slice(n, T)):
+        part = lm.token_logprobs(x[r], t[r], scale=0.9, top=top)
+        for k in out:
+            assert torch.equal(out[k][r], part[k]), k
