@@ -48,7 +48,8 @@ GEMM_SOURCES = ("quantize_grouped_gemm_amd/csrc/mx_gemm.hip", "quantize_grouped_
 
 def gemm_source_hash():
     """Hash of the GEMM kernel's code and build flags. Comments and blank
-    lines of the C++ sources are left out, so editing a comment keeps the
+    lines of the C++ sources are left out, and of the build file all but the
+    target and the flags, so editing a comment or adding a source keeps the
     counters taken on the same code valid."""
     import hashlib
     import re
@@ -56,7 +57,9 @@ def gemm_source_hash():
     for rel in GEMM_SOURCES:
         with open(os.path.join(ROOT, rel), "rb") as f:
             text = f.read()
-        if not rel.endswith(".py"):
+        if rel.endswith(".py"):
+            text = b"".join(re.findall(rb"^ARCH = .*?\n|^FLAGS = \[.*?^\]\n", text, flags=re.S | re.M))
+        else:
             code = re.sub(rb"/\*.*?\*/", b"", text, flags=re.S)
             code = re.sub(rb"//[^\n]*", b"", code)
             text = b"\n".join(line.rstrip() for line in code.split(b"\n") if line.strip())

@@ -22,6 +22,7 @@
 
 #include "mx_device.h"
 #include "mx_kernels.h"
+#include "mx_swiglu.h"
 #include "mx_tile.h"
 
 #include <algorithm>

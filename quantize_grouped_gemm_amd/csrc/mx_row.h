@@ -5,6 +5,7 @@
 #pragma once
 
 #include "mx_device.h"
+#include "mx_lm_device.h"
 #include "mx_tile.h"
 
 namespace mxk {

@@ -19,6 +19,7 @@
 #include "mx_fmt.h"
 #include "mx_lm.h"
 #include "mx_row.h"
+#include "mx_swiglu.h"
 #include "mx_tile.h"
 
 namespace mxk {
