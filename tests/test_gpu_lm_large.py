@@ -121,3 +121,65 @@ def test_scoring(gpu, T, V, dtype, top):
         part = lm.token_logprobs(x[r], t[r], scale=0.9, top=top)
         for k in out:
             assert torch.equal(out[k][r], part[k]), k
+
+
+def _normal(shape, std, g):
+    return torch.empty(shape, dtype=BF, device=dev()).normal_(0, std, generator=g)
+
+
+@pytest.mark.parametrize("T,C", [(140032, 16384)])
+def test_norm_past_32_bits(gpu, T, C):
+    """More than 2^31 elements: the last rows equal a call of their own."""
+    g = torch.Generator(device=dev()).manual_seed(1)
+    x, w = _normal((T, C), 1.0, g), torch.ones(C, device=dev())
+    out = lm.add_rmsnorm_quant(x, w, colwise=True, checkpoint=True)
+    bwd = lm.add_rmsnorm_bwd(x, w, out["rstd"], checkpoint=(out["q_ck"], out["s_ck"]), colwise=True)
+    r0 = T - 640
+    part = lm.add_rmsnorm_quant(x[r0:], w, colwise=True, checkpoint=True)
+    pb = lm.add_rmsnorm_bwd(x[r0:], w, part["rstd"], checkpoint=(part["q_ck"], part["s_ck"]), colwise=True)
+    for whole, piece, rows, codes in ((out, part, ("rstd",), ("q_row", "q_ck")), (bwd, pb, ("dx",), ("q_row",))):
+        for k in rows + codes:
+            _eq(whole[k][r0:], piece[k], k)
+        for k in codes:
+            s = k.replace("q_", "s_")
+            _eq(whole[s][:, r0:], piece[s], s)
+        _eq(whole["q_col"][:, r0:], piece["q_col"], "q_col")
+        _eq(whole["s_col"][r0 // 128:], piece["s_col"], "s_col")
+
+
+@pytest.mark.parametrize("T,H", [(70016, 16384)])
+def test_swiglu_past_32_bits(gpu, T, H):
+    g = torch.Generator(device=dev()).manual_seed(2)
+    z, dh = _normal((T, 2 * H), 1.5, g), _normal((T, H), 1e-2, g)
+    out = lm.swiglu_ckpt_fwd(z[:, :H], z[:, H:])
+    bwd = lm.swiglu_ckpt_bwd(dh, out["q_ck"], out["s_ck"])
+    r0 = T - 640
+    part = lm.swiglu_ckpt_fwd(z[r0:, :H], z[r0:, H:])
+    pb = lm.swiglu_ckpt_bwd(dh[r0:], part["q_ck"], part["s_ck"])
+    for whole, piece, codes in ((out, part, ("q_row", "q_ck")), (bwd, pb, ("q_row",))):
+        for k in codes:
+            s = k.replace("q_", "s_")
+            _eq(whole[k][r0:], piece[k], k)
+            _eq(whole[s][:, r0:], piece[s], s)
+        _eq(whole["q_col"][:, r0:], piece["q_col"], "q_col")
+        _eq(whole["s_col"][r0 // 128:], piece["s_col"], "s_col")
+
+
+@pytest.mark.parametrize("T,V,pad", [(17024, 131072, 0), (17024, 130001, 4)])
+def test_logits_past_32_bits(gpu, T, V, pad):
+    """Aligned rows, and rows of an odd vocabulary further apart."""
+    g = torch.Generator(device=dev()).manual_seed(3)
+    x = _normal((T, V + pad), 2.5, g)[:, :V]
+    t = torch.randint(0, V, (T,), generator=g, device=dev())
+    dl = torch.randn(T, generator=g, device=dev()) / T
+    out = lm.token_logprobs(x, t, top=5)
+    bwd = lm.token_logprobs_bwd(x, t, out["stats"], out["entropy"], dl, dl)
+    r0 = T - 640
+    part = lm.token_logprobs(x[r0:], t[r0:], top=5)
+    pb = lm.token_logprobs_bwd(x[r0:], t[r0:], part["stats"], part["entropy"], dl[r0:], dl[r0:])
+    for k in out:
+        _eq(out[k][r0:], part[k], k)
+    _eq(bwd["q_row"][r0:], pb["q_row"], "q_row")
+    _eq(bwd["s_row"][:, r0:], pb["s_row"], "s_row")
+    _eq(bwd["q_col"][:, r0:], pb["q_col"], "q_col")
+    _eq(bwd["s_col"][r0 // 128:], pb["s_col"], "s_col")
