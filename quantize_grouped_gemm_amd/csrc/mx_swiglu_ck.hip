@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kFmtThreads) void k_swiglu_ck_fwd(SwigluPack pack) 
   __shared__ uint32_t s_ck[2][kTR];
   const SwigluCkArgs a = pack.wide<F>();
   const TilePos at = tile_pos(blockIdx.x, (uint32_t)((a.hidden + kTC - 1) / kTC), (uint32_t)((a.rows_pad + kTR - 1) / kTR),
-                              a.bands);
+                              false);
   const int64_t r0 = at.r0, c0 = at.c0;
   const int rows_valid = (int)min<int64_t>(kTR, a.rows - r0);
   const int rows_pad = (int)min<int64_t>(kTR, a.rows_pad - r0);
@@ -156,13 +156,9 @@ __global__ __launch_bounds__(kFmtThreads) void k_swiglu_ck_bwd(SwigluPack pack) 
     swiglu_ck_bwd_tile<F, false>(a, l, r0, c0, rows_valid, rows_pad, cols_valid);
 }
 
-// Bands (tile_pos) from 8192 rows on: 8192 x 14336 backward 220 -> 202 us,
-// 12345 x 4096 backward 85 -> 80, 16384 x 6912 forward 193 -> 185 (8192 x 8192
-// backward 120 -> 128); with fewer rows they cost 1 to 4% (5000 x 11008
-// backward 90 against 94).
-static SwigluPack pack(const SwigluCkArgs& a, const uint16_t* in, int64_t ld) {
+static SwigluPack pack(const SwigluCkArgs& a, const uint16_t* in, int64_t ld, bool bands) {
   return SwigluPack{in, a.b, a.q_row, a.s_row, a.q_col, a.s_col, a.q_ck, a.s_ck, (int32_t)ld, (int32_t)a.rows,
-                    (int32_t)a.hidden, a.rows_pad >= 64 * kTR};
+                    (int32_t)a.hidden, bands};
 }
 
 static dim3 tile_grid(const SwigluCkArgs& a) {
@@ -170,15 +166,23 @@ static dim3 tile_grid(const SwigluCkArgs& a) {
 }
 
 hipError_t launch_swiglu_ck_fwd(const SwigluCkArgs& a, hipStream_t s) {
-  const SwigluPack p = pack(a, a.a, a.ld_ab);
+  const SwigluPack p = pack(a, a.a, a.ld_ab, false);
   with_fmt(a.rceil, a.k128, [&](auto f) {
     hipLaunchKernelGGL(k_swiglu_ck_fwd<decltype(f)>, tile_grid(a), dim3(kFmtThreads), 0, s, p);
   });
   return hipGetLastError();
 }
 
+// Bands (tile_pos) in the backward of many tiles of long rows: 8192 x 9216 135 -> 124
+// us, 8192 x 14336 206 -> 191, 16384 x 6912 191 -> 182, 4096 x 28672 214 -> 192
+// (8192 x 11008 148 -> 150, 12288 x 8192 172 -> 176). Fewer tiles or shorter rows are
+// slower in bands (4096 x 8192 55 -> 59, 8192 x 8192 110 -> 117, 32768 x 2560 142 ->
+// 157), and so is the forward (8192 x 8192 97 -> 104, 8192 x 14336 189.5 -> 192.3,
+// 16384 x 6912 184 -> 183).
+static bool grad_bands(const SwigluCkArgs& a) { return tile_grid(a).x > 4096 && a.hidden > 4096; }
+
 hipError_t launch_swiglu_ck_bwd(const SwigluCkArgs& a, hipStream_t s) {
-  const SwigluPack p = pack(a, a.dh, a.ld_dh);
+  const SwigluPack p = pack(a, a.dh, a.ld_dh, grad_bands(a));
   with_fmt(a.rceil, a.k128, [&](auto f) {
     hipLaunchKernelGGL(k_swiglu_ck_bwd<decltype(f)>, tile_grid(a), dim3(kFmtThreads), 0, s, p);
   });

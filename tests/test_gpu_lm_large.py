@@ -183,3 +183,26 @@ def test_logits_past_32_bits(gpu, T, V, pad):
     _eq(bwd["s_row"][:, r0:], pb["s_row"], "s_row")
     _eq(bwd["q_col"][:, r0:], pb["q_col"], "q_col")
     _eq(bwd["s_col"][r0 // 128:], pb["s_col"], "s_col")
+
+
+@pytest.mark.parametrize("T,H,layout", [(8300, 8320, "k128"), (9001, 7712, "plain")])
+def test_swiglu_tile_orders(gpu, T, H, layout):
+    """More than 4096 tiles of long rows: the backward walks them in another order."""
+    g = torch.Generator(device=dev()).manual_seed(4)
+    z, dh = _normal((T, 2 * H), 1.5, g), _normal((T, H), 1e-2, g)
+    out = lm.swiglu_ckpt_fwd(z[:, :H], z[:, H:], layout=layout)
+    bwd = lm.swiglu_ckpt_bwd(dh, out["q_ck"], out["s_ck"], layout=layout)
+    for r0 in range(0, T, 4096):
+        r1 = min(r0 + 4096, T)
+        part = lm.swiglu_ckpt_fwd(z[r0:r1, :H], z[r0:r1, H:], layout=layout)
+        pb = lm.swiglu_ckpt_bwd(dh[r0:r1], part["q_ck"], part["s_ck"], layout=layout)
+        cols = slice(r0, r0 + lm.padded_rows(r1 - r0, layout))
+        for whole, piece, codes in ((out, part, ("q_row", "q_ck")), (bwd, pb, ("q_row",))):
+            for k in codes:
+                s = k.replace("q_", "s_")
+                _eq(whole[k][r0:r1], piece[k], (k, r0))
+                _eq(whole[s][:, r0:r1] if layout == "k128" else whole[s][r0:r1], piece[s], (s, r0))
+            _eq(whole["q_col"][:, cols], piece["q_col"], ("q_col", r0))
+            step = 128 if layout == "k128" else 32
+            blocks = slice(cols.start // step, cols.stop // step)
+            _eq(whole["s_col"][blocks] if layout == "k128" else whole["s_col"][:, blocks], piece["s_col"], ("s_col", r0))
