@@ -108,9 +108,10 @@ int64_t mx_token_logprobs_work(int64_t rows, int64_t vocab, int32_t top);
  *   entropy  float32 [rows]: ls - sum_j p_j d_j
  *   top_logp float32, top_idx int32 [rows, top]: the `top` largest x in
  *            descending order, ties to the lower index (top = 0: both NULL)
- * Entries of -infinity are ruled out (p = 0). A row with nothing left has
- * entropy 0, ls = -infinity and logp = -infinity; a NaN or +infinity makes its
- * row's results NaN (top_idx stays within the vocabulary).
+ * ls and entropy are never below 0, logp and top_logp never above it. Entries of
+ * -infinity are ruled out (p = 0). A row with nothing left has entropy 0,
+ * ls = -infinity and logp = -infinity; a NaN or +infinity makes its row's results
+ * NaN (top_idx: distinct tokens all the same, those with NaN first).
  * 1 <= vocab < 2^31 - 2^16, 0 <= top <= min(64, vocab); scale in
  * [1e-6, 1e6]. A target outside [0, vocab) that is not ignore_index is
  * treated as not scored and sets bit 3 of *dev_err if that is non-NULL.

@@ -128,7 +128,8 @@ __device__ __forceinline__ uint2 chunk_codes(uint4 v, uint32_t sb) {
 }
 
 // The thread's chunks of the bf16 tile whose (0,0) is `base` (uniform), row
-// stride ld < 2^27; zeros outside the valid region.
+// stride ld <= 2^26 (31 rows of 2^27 bytes fit the lanes' 32-bit offsets); zeros
+// outside the valid region.
 template <bool FULL>
 __device__ __forceinline__ void fmt_load(uint4 (&v)[kChunks], const uint16_t* base, int64_t ld, int rows_valid,
                                          int cols_valid) {

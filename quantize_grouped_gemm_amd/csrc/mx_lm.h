@@ -64,7 +64,7 @@ struct LogprobArgs {
 };
 
 // A launch costs the host 2.8 us with up to 112 bytes of kernel arguments and 3.4
-// with more, of the 8 to 10 us that a small call takes: kernels get their blocks
+// with more, of the 4 to 10 us that a small call takes: kernels get their blocks
 // packed (sizes in 32 bits, what follows from others left out) and widen them,
 // and none reads the grid's or the workgroup's size, which would add 256 bytes.
 constexpr size_t kArgBytes = 112;

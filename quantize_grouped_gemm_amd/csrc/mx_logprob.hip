@@ -753,8 +753,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobPack pack)
 //
 // The kernel is as close to its VALU issue rate as to HBM's: these 11 slots a
 // logit (4 of them v_exp_f32) in place of 14, with c's correction and the scaling
-// by 2^n as instructions of their own, take 4096 x 131072 from 429 to 407 us
-// (5.4 TB/s) and 6000 x 100001 from 588 to 565.
+// by 2^n as instructions of their own, took 4096 x 131072 from 429 to 407 us (399
+// now, 5.5 TB/s).
 //
 // The exponent field holds n + up, and the constants the factor 2^-up; x is
 // bounded below where n + up is -122, so that a masked entry stays a number. up
@@ -1050,10 +1050,10 @@ hipError_t launch_logprob_fwd(const LogprobArgs& a, hipStream_t s) {
 
 // Bands (tile_pos) for large gradients whose rows are aligned: their pitch
 // sends the 128 rows of a tile to few memory channels at a time, and eight
-// bands spread that. 4096 x 131072 498 -> 452 us, 8192 x 65536 490 -> 436,
-// 4096 x 50304 float32 265 -> 248; without it smaller gradients are faster
-// (8192 x 16384 116 against 132 us, 2048 x 131072 float32 310 against 327), and
-// so are unaligned rows (6000 x 100001 489 against 528).
+// bands spread that. 4096 x 131072 495 -> 399 us, 8192 x 65536 509 -> 398,
+// 4096 x 50304 float32 246 -> 244; without it smaller gradients are faster
+// (8192 x 16384 107 against 124 us, 2048 x 131072 float32 295 against 318), and
+// so are unaligned rows (6000 x 100001 457 against 509).
 static bool aligned_rows(const LogprobArgs& a) {
   return a.ld * (a.f32 ? 4 : 2) % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
 }
@@ -1063,12 +1063,12 @@ static bool grad_bands(const LogprobArgs& a, int64_t nx, int64_t ny) {
 }
 
 // Where each direction's codes are past what the 256 MB Infinity Cache can hold
-// for the head's gradient GEMMs, both go past it: 4096 x 131072 456 -> 445 us;
-// and so do the logits, read here for the last time, where no line is shared by
-// two tiles: 445 -> 429 (6000 x 100001, unaligned, 588 against 605 with them).
-// Below that size only the row-wise codes do: 333 x 50001 float32 28.2 -> 27.2
-// us; with both 26.4, but the two GEMMs behind it then take 3 us longer (7 us
-// behind 1000 x 32000).
+// for the head's gradient GEMMs, both go past it: 4096 x 131072 434 -> 425 us; and
+// so do the logits, read here for the last time, where no line is shared by two
+// tiles: 425 -> 399 (6000 x 100001, unaligned, 457 against 552 with them). Below that
+// size only the row-wise codes do: 333 x 50001 float32 24.2 -> 22.8 us, 1000 x 32000
+// 32.2 -> 31.5; the column-wise ones gain the kernel nothing more (22.8), and cost
+// the two GEMMs behind it 3 us (7 us behind 1000 x 32000).
 static GradKind grad_kind(const LogprobArgs& a) {
   if (a.rows_pad * a.vocab_pad <= (1ll << 28)) return kGradSmall;
   return aligned_rows(a) ? kGradStream : kGradLarge;

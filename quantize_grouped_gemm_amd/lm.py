@@ -8,13 +8,18 @@ MXFP8 transformer runs between its GEMMs.
 Like the functions of mx: arguments are checked against the sizes that go with
 them, outputs are allocated with torch unless given in `out`, the library is
 called on torch's current stream, and there is no fallback. Calls without
-given outputs go through _lmhost (C++), which takes about 6 us of host time
-where the steps below take 15 to 25; what it does not take as it is (given
-outputs, arguments to refuse) comes back and is checked here. Codes and scales
-are uint8 tensors under the keys q_row / s_row, q_col / s_col, q_ck / s_ck in
-the layouts of mx.quantize. The number of rows T is free; column-wise codes
-cover padded_rows(T, layout) rows, the ones past T being zeros, so they feed
-mx.scaled_mm as they are.
+given outputs go through _lmhost (C++), which takes 4 to 10 us of host time
+where the steps below take 11 to 21; its checks are these in short, and what it
+does not take as it is (given outputs, arguments to refuse) comes back and is
+checked here, with a message. Without a built _lmhost.so such calls are refused.
+It allocates what belongs together at once: codes and their scales, and the
+outputs of token_logprobs, are slices of one allocation, so keeping or saving one
+of them keeps the memory of all (outputs made here have one each).
+
+Codes and scales are uint8 tensors under the keys q_row / s_row, q_col / s_col,
+q_ck / s_ck in the layouts of mx.quantize. The number of rows T is free;
+column-wise codes cover padded_rows(T, layout) rows, the ones past T being zeros,
+so they feed mx.scaled_mm as they are.
 """
 
 import ctypes
