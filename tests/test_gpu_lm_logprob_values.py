@@ -217,3 +217,23 @@ def test_gradients_of_any_size(gpu, dtype, which):
     gone = torch.nn.functional.pad(x == -INF, (0, Vp - V), value=True)
     gone[torch.arange(T), t] = False
     assert not (out["q_row"] & 0x7F)[gone].any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,V", [(300, 30001), (300, 131072), (100, 131072)])
+@pytest.mark.parametrize("lo,hi", [(7.0, 9.0), (2.0, 4.0)])
+def test_scoring_of_sure_rows(gpu, T, V, dtype, lo, hi):
+    """Rows whose target holds all but e^-lo .. e^-hi of the probability. S, between
+    1 and 2, passes at most 32 roundings within a tile, 32 over a thread's tiles and 10
+    where threads are joined, each at most 2^-24 and of either sign: sqrt(74) 2^-24 =
+    5e-7 root mean square, and as much in ls. A holds the best token's term times at
+    most 8.5: roundings up to 2^-21, 4.1e-6 in A / S, 2.9e-6 in the entropy times ln 2,
+    next to those of ls."""
+    x, t = _sure_rows(T, V, dtype, 1.0, lo, hi, V)
+    out = lm.token_logprobs(x, t)
+    x64 = x.cpu().to(F64)
+    _, ls, logp, ent = R.logprob_fwd(x64, t.cpu(), 1.0)
+    rms = {k: float((got.cpu().to(F64) - want).square().mean().sqrt())
+           for k, got, want in (("ls", out["stats"][:, 1], ls), ("logp", out["logp"], logp), ("entropy", out["entropy"], ent))}
+    print(f"T={T} V={V} {dtype} {lo}: {rms}", flush=True)
+    assert rms["ls"] <= 5.2e-7 and rms["logp"] <= 5.2e-7 and rms["entropy"] <= 3.0e-6
