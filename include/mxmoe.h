@@ -67,7 +67,9 @@ mx_status mx_route(const void* x, mx_dtype x_dtype, int64_t ld, int64_t rows,
 
 /* Gradient of mx_route's weights with respect to x (the choice and the bias
  * have none): dlogits [rows, experts] of x_dtype, contiguous. idx is the
- * forward's; an entry outside [0, experts) has no part. */
+ * forward's; an entry outside [0, experts) has no part, nor has one whose score is 0
+ * as a float32 (a sigmoid's logit below about -104): its weight is 0 whatever the logit, and
+ * a row of such scores only gets zeros. */
 mx_status mx_route_bwd(const void* x, mx_dtype x_dtype, int64_t ld, int64_t rows,
                        int32_t experts, mx_score score, const int32_t* idx,
                        int32_t top, int renorm, float scale,

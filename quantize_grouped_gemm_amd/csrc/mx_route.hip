@@ -330,7 +330,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, bool vec) 
 
 // Gradient of the weights with respect to the logits: the scores are formed
 // again as above, the rest is in float64 too (the terms cancel where one
-// expert has nearly all the weight).
+// expert has nearly all the weight). Chosen scores that are 0 as float32 have no part.
 template <int LPT, int PER, bool F32>
 __global__ __launch_bounds__(kRouteThreads) void k_route_bwd(RouteArgs a, bool vec, bool vec_out) {
   constexpr int kTokens = kRouteThreads / LPT;
@@ -367,7 +367,14 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_bwd(RouteArgs a, bool v
         const double t64 = (double)xi - m;
         s = xi == -INFINITY ? 0.0 : exp64(t64 < -700.0 ? -700.0 : t64, pow2) * inv;
       }
-      d = (double)a.dweights[row * a.top + lane] * (double)a.scale;
+      // a score that is 0 as a float32 gave a weight of 0, also where all of a row's are and "a sum of 0 divides by
+      // 1": in float64 it would still have a share of their sum
+      if ((float)s == 0.0f) {
+        idx = -1;
+        s = 0;
+      } else {
+        d = (double)a.dweights[row * a.top + lane] * (double)a.scale;
+      }
     }
   }
   if (a.renorm) {

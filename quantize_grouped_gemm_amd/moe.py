@@ -120,7 +120,8 @@ def route(x, top, bias=None, score="softmax", groups=1, top_groups=1, group_scor
 
 def route_bwd(x, idx, dweights, score="softmax", renorm=True, scale=1.0, out=None):
     """Gradient of route's weights with respect to x: idx is the forward's,
-    dweights float32 [T, top]. Returns [T, E] of x's type."""
+    dweights float32 [T, top]. Choices whose score is 0 as a float32 have no part.
+    Returns [T, E] of x's type."""
     if out is None:
         res = _done((_host or host()).route_bwd(x, idx, dweights, score, renorm, scale), "mx_route_bwd")
         if res is not None:
