@@ -153,10 +153,11 @@ mx_status mx_b128_quantize_weight(const void* w, int64_t batch, int64_t rows,
  * [K/128, N] (block_b = 0) or [K/128, ceil(N/128)] (block_b = 1). C [M, N] of
  * out_dtype, row stride ldo elements (rows 16-byte aligned). K a multiple of 128
  * (K = 0 gives zeros), N of 8. Any M; few rows take a kernel that streams B.
- * Here and below a row of codes is shorter than 2^23 and one matrix's scales are
- * fewer than 2^29. The matrix unit holds a group of 8 products to 2^-13 of its
- * largest: float32 results are off by some 1.5e-5 of their size. The scales of the
- * two sides are multiplied in float32. */
+ * Here and below a row of codes is shorter than 2^23, one matrix's scales are fewer
+ * than 2^29, and a launch takes fewer than 2^22 tiles of 256 x 256 results a group
+ * (64 x 128 in grouped products of fewer than 128 rows a group). The matrix unit
+ * holds a group of 8 products to 2^-13 of its largest: float32 results are off by some
+ * 1.5e-5 of their size. The scales of the two sides are multiplied in float32. */
 mx_status mx_b128_mm(const uint8_t* qa, const float* sa, const uint8_t* qb,
                      const float* sb, int block_b, int64_t M, int64_t N,
                      int64_t K, mx_dtype out_dtype, void* out, int64_t ldo,

@@ -797,16 +797,17 @@ static void with_out(const B128GemmArgs& a, Fn f) {
   }
 }
 
-hipError_t launch_b128_mm(const B128GemmArgs& a, hipStream_t s) {
-  if (a.M == 0 || a.N == 0) return hipSuccess;
+// The variant of a dense product: f(shape, whether it is a split one, its workgroups).
+template <class Fn>
+static auto with_mm(const B128GemmArgs& a, Fn f) {
+  auto tiles = [&](auto shape) {
+    using S = decltype(shape);
+    return ((a.M + S::BM - 1) / S::BM) * ((a.N + S::BN - 1) / S::BN);
+  };
   auto split = [&](auto shape) {
     using S = decltype(shape);
     const int64_t mt = (a.M + S::BM - 1) / S::BM, nt = (a.N + S::BN - 1) / S::BN;
-    with_out(a, [&](auto rowb, auto f32) {
-      hipLaunchKernelGGL((k_b128_split<S, rowb, f32>), dim3((unsigned)(mt * ((nt + 7) / 8 * 8))), dim3(S::threads), 0, s, a,
-                         (int)mt);
-    });
-    return hipGetLastError();
+    return f(shape, std::true_type{}, mt * ((nt + 7) / 8 * 8));
   };
   if (a.K > 0 && a.M <= 64) {
     if (a.M <= 16 && a.N <= 2 * kFewColumns) return split(Few<1>{});
@@ -815,36 +816,40 @@ hipError_t launch_b128_mm(const B128GemmArgs& a, hipStream_t s) {
     if (a.M <= 16 && a.N > kMidColumns && a.N < 2 * kWideColumns) return split(FewWide{});
     if (a.N < kWideColumns) return split(Mid{});
   }
-  auto tiles = [&](auto shape) {
-    using S = decltype(shape);
-    return ((a.M + S::BM - 1) / S::BM) * ((a.N + S::BN - 1) / S::BN);
-  };
   // more rows: split tiles while the card takes them all at once, large ones from half of the CUs on. us of Mid /
   // Mid2 / Small / Big: 256 x 4096 x 7168 17, 26, 32, 81; 512 x 4096 x 7168 32, 27, 34, 82; 512 x 7168 x 2048 25, 20,
   // 15, 29; 1024 x 4096 x 7168 64, 53, 41, 82; 2304 x 4096 x 7168 -, -, 88, 83; 1536 x 7168 x 2048 -, -, 36, 31.
   if (a.K > 0 && tiles(Mid{}) <= kCUs) return split(Mid{});
   if (a.K > 0 && tiles(Mid2{}) <= kCUs) return split(Mid2{});
-  if (tiles(Big{}) > kCUs / 2) {
-    with_out(a, [&](auto rowb, auto f32) {
-      hipLaunchKernelGGL((k_b128_mm<Big, rowb, f32>), dim3((unsigned)tiles(Big{})), dim3(Big::threads), 0, s, a);
-    });
-  } else {
-    with_out(a, [&](auto rowb, auto f32) {
-      hipLaunchKernelGGL((k_b128_mm<Small, rowb, f32>), dim3((unsigned)tiles(Small{})), dim3(Small::threads), 0, s, a);
-    });
-  }
-  return hipGetLastError();
+  if (tiles(Big{}) > kCUs / 2) return f(Big{}, std::false_type{}, tiles(Big{}));
+  return f(Small{}, std::false_type{}, tiles(Small{}));
 }
 
-hipError_t launch_b128_grouped(const B128GemmArgs& a, hipStream_t s) {
+int64_t b128_mm_grid(const B128GemmArgs& a) {
+  return with_mm(a, [](auto, auto, int64_t n) { return n; });
+}
+
+hipError_t launch_b128_mm(const B128GemmArgs& a, hipStream_t s) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
-  const int64_t active = std::min<int64_t>(a.E, a.M);
-  auto split = [&](auto shape) {
+  return with_mm(a, [&](auto shape, auto split, int64_t n) {
     using S = decltype(shape);
-    const int64_t nt = (a.N + S::BN - 1) / S::BN;
-    hipLaunchKernelGGL(k_b128_split_grouped<S>, dim3((unsigned)((active + 1) * nt)), dim3(S::threads), 0, s, a, (int)nt);
+    with_out(a, [&](auto rowb, auto f32) {
+      if constexpr (decltype(split)::value)
+        hipLaunchKernelGGL((k_b128_split<S, rowb, f32>), dim3((unsigned)n), dim3(S::threads), 0, s, a,
+                           (int)((a.M + S::BM - 1) / S::BM));
+      else
+        hipLaunchKernelGGL((k_b128_mm<S, rowb, f32>), dim3((unsigned)n), dim3(S::threads), 0, s, a);
+    });
     return hipGetLastError();
-  };
+  });
+}
+
+// The same for a grouped product, whose workgroups are n for each column tile.
+template <class Fn>
+static auto with_grouped(const B128GemmArgs& a, Fn f) {
+  const int64_t active = std::min<int64_t>(a.E, a.M);
+  auto split = [&](auto shape) { return f(shape, std::true_type{}, active + 1); };
+  auto whole = [&](auto shape) { return f(shape, std::false_type{}, a.M / decltype(shape)::BM + active + 1); };
   const int64_t columns = active * a.N;
   if (a.M <= 64 * active) {
     if (a.M <= 16 * active && columns <= 2 * kFewColumns) return split(Few<1>{});
@@ -853,26 +858,39 @@ hipError_t launch_b128_grouped(const B128GemmArgs& a, hipStream_t s) {
     if (a.M <= 4 * active && columns > kMidColumns && columns < 2 * kWideColumns) return split(FewWide{});
     if (columns < kWideColumns) return split(Mid{});
   }
-  auto go = [&](auto shape) {
-    using S = decltype(shape);
-    const int64_t mt = a.M / S::BM + active + 1, nt = (a.N + S::BN - 1) / S::BN;
-    hipLaunchKernelGGL(k_b128_grouped<S>, dim3((unsigned)(mt * nt)), dim3(S::threads), 0, s, a, (int)mt);
-  };
   // Large tiles for 128 rows a group and more, if they give half of the CUs one, and some more rows where they give
   // no more than that. us of Small / Big: 32 x 128 x 4096 x 7168 254, 221; 32 x 100 x 7168 x 2048 122, 128; 8 x 128 x
   // 4096 x 7168 66, 87; 8 x 256 x 4096 x 7168 122, 98; 8 x 128 x 7168 x 2048 40, 34; 32 x 256 x 768 x 2048 22, 31;
   // 8 x 512 x 1536 x 7168 82, 92; 8 x 768 x 1536 x 7168 114, 92.
   const int64_t large = std::max(active, a.M / Big::BM) * ((a.N + Big::BN - 1) / Big::BN);
-  if (a.M >= 128 * active && large >= kCUs / 2 && a.M / active * large >= 160 * (kCUs / 2)) go(Big{});
-  else go(Small{});
-  return hipGetLastError();
+  if (a.M >= 128 * active && large >= kCUs / 2 && a.M / active * large >= 160 * (kCUs / 2)) return whole(Big{});
+  return whole(Small{});
+}
+
+int64_t b128_grouped_grid(const B128GemmArgs& a) {
+  return with_grouped(a, [&](auto shape, auto, int64_t n) { return n * ((a.N + shape.BN - 1) / shape.BN); });
+}
+
+hipError_t launch_b128_grouped(const B128GemmArgs& a, hipStream_t s) {
+  if (a.M == 0 || a.N == 0) return hipSuccess;
+  return with_grouped(a, [&](auto shape, auto split, int64_t n) {
+    using S = decltype(shape);
+    const int64_t nt = (a.N + S::BN - 1) / S::BN;
+    const dim3 grid((unsigned)(n * nt));
+    if constexpr (decltype(split)::value) hipLaunchKernelGGL(k_b128_split_grouped<S>, grid, dim3(S::threads), 0, s, a, (int)nt);
+    else hipLaunchKernelGGL(k_b128_grouped<S>, grid, dim3(S::threads), 0, s, a, (int)n);
+    return hipGetLastError();
+  });
+}
+
+int64_t b128_wgrad_grid(const B128GemmArgs& a) {
+  return a.E * ((a.M + Big::BM - 1) / Big::BM) * ((a.N + Big::BN - 1) / Big::BN);
 }
 
 hipError_t launch_b128_wgrad(const B128GemmArgs& a, hipStream_t s) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   using S = Big;
-  const int64_t mt = (a.M + S::BM - 1) / S::BM, nt = (a.N + S::BN - 1) / S::BN;
-  const dim3 grid((unsigned)(a.E * mt * nt)), block(S::threads);
+  const dim3 grid((unsigned)b128_wgrad_grid(a)), block(S::threads);
   if (a.out_f32) hipLaunchKernelGGL((k_b128_wgrad<S, true>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((k_b128_wgrad<S, false>), grid, block, 0, s, a);
   return hipGetLastError();

@@ -85,6 +85,10 @@ struct B128GemmArgs {
   int32_t E;
   int32_t* dev_err;
 };
+// Workgroups (of at most 512 threads) that the launches below take.
+int64_t b128_mm_grid(const B128GemmArgs& a);
+int64_t b128_grouped_grid(const B128GemmArgs& a);
+int64_t b128_wgrad_grid(const B128GemmArgs& a);
 hipError_t launch_b128_mm(const B128GemmArgs& a, hipStream_t s);
 hipError_t launch_b128_grouped(const B128GemmArgs& a, hipStream_t s);
 hipError_t launch_b128_wgrad(const B128GemmArgs& a, hipStream_t s);

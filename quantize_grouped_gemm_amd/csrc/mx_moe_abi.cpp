@@ -101,9 +101,9 @@ mx_status check_groups(const char* fn, const int32_t* offs, int32_t E, int64_t c
   return MX_OK;
 }
 
-// Tiles of a product, at their smallest (64 x 128, or 16 columns of few rows).
-mx_status check_tiles(const char* fn, int64_t row_tiles, int64_t N) {
-  MX_REQUIRE(row_tiles * ((N + 15) / 16) <= kMaxTiles, MX_ERR_SHAPE, "%s: too many tiles for one launch", fn);
+// Workgroups of a product's launch.
+mx_status check_grid(const char* fn, int64_t workgroups) {
+  MX_REQUIRE(workgroups < kMaxTiles, MX_ERR_SHAPE, "%s: too many tiles for one launch", fn);
   return MX_OK;
 }
 
@@ -300,8 +300,11 @@ mx_status mx_b128_mm(const uint8_t* qa, const float* sa, const uint8_t* qb, cons
   MX_REQUIRE(M >= 0 && M < kMaxIndex && N >= 0 && N < kMaxIndex && N % 8 == 0 && K >= 0 && K % 128 == 0, MX_ERR_SHAPE,
              "%s: M (%lld), N (%lld, a multiple of 8), K (%lld, a multiple of 128)", fn, (long long)M, (long long)N,
              (long long)K);
-  MX_CHECK(check_tiles(fn, (M + 63) / 64, N));
   if (M == 0 || N == 0) return MX_OK;
+  mxk::B128GemmArgs a{};
+  a.qa = qa; a.qb = qb; a.sa = sa; a.sb = sb; a.M = M; a.N = N; a.K = K; a.ldo = ldo;
+  a.block_b = block_b != 0; a.out_f32 = out_dtype == MX_F32; a.out = out;
+  MX_CHECK(check_grid(fn, mxk::b128_mm_grid(a)));
   if (K) {
     MX_CHECK(check_operand(fn, "A", qa, sa, K, K / 128 * M));
     MX_CHECK(check_operand(fn, "B", qb, sb, K, K / 128 * (block_b ? (N + 127) / 128 : N)));
@@ -310,9 +313,6 @@ mx_status mx_b128_mm(const uint8_t* qa, const float* sa, const uint8_t* qb, cons
   MX_REQUIRE(al16(out) && ldo >= N && ldo % (out_dtype == MX_F32 ? 4 : 8) == 0, MX_ERR_ALIGN,
              "%s: output rows must be 16-byte aligned and ldo (%lld) >= N", fn, (long long)ldo);
   MX_DEVICE();
-  mxk::B128GemmArgs a{};
-  a.qa = qa; a.qb = qb; a.sa = sa; a.sb = sb; a.M = M; a.N = N; a.K = K; a.ldo = ldo;
-  a.block_b = block_b != 0; a.out_f32 = out_dtype == MX_F32; a.out = out;
   return launched(mxk::launch_b128_mm(a, as_stream(stream)), fn);
 }
 
@@ -322,16 +322,16 @@ mx_status mx_b128_grouped_mm(const uint8_t* qa, const float* sa, const uint8_t* 
   MX_CHECK(check_groups(fn, offs, E, cap));
   MX_REQUIRE(N >= 0 && N % 8 == 0 && N < kMaxIndex && K > 0 && K % 128 == 0, MX_ERR_SHAPE,
              "%s: N (%lld) must be a multiple of 8, K (%lld) a positive multiple of 128", fn, (long long)N, (long long)K);
-  MX_CHECK(check_tiles(fn, cap / 64 + std::min<int64_t>(E, cap) + 1, N));
   if (cap == 0 || N == 0) return MX_OK;
+  mxk::B128GemmArgs a{};
+  a.qa = qa; a.qb = qw; a.sa = sa; a.sb = sw; a.M = cap; a.N = N; a.K = K; a.ldo = N;
+  a.block_b = true; a.out = out; a.offs = offs; a.E = E; a.dev_err = dev_err;
+  MX_CHECK(check_grid(fn, mxk::b128_grouped_grid(a)));
   MX_CHECK(check_operand(fn, "A", qa, sa, K, K / 128 * cap));
   MX_CHECK(check_operand(fn, "B", qw, sw, K, K / 128 * ((N + 127) / 128)));
   MX_REQUIRE(out, MX_ERR_NULL, "%s: out is NULL", fn);
   MX_REQUIRE(al16(out) && al4(dev_err), MX_ERR_ALIGN, "%s: out must be 16-byte and dev_err 4-byte aligned", fn);
   MX_DEVICE();
-  mxk::B128GemmArgs a{};
-  a.qa = qa; a.qb = qw; a.sa = sa; a.sb = sw; a.M = cap; a.N = N; a.K = K; a.ldo = N;
-  a.block_b = true; a.out = out; a.offs = offs; a.E = E; a.dev_err = dev_err;
   return launched(mxk::launch_b128_grouped(a, as_stream(stream)), fn);
 }
 
@@ -345,7 +345,10 @@ mx_status mx_b128_grouped_mm_wgrad(const uint8_t* qg, const float* sg, const uin
   MX_REQUIRE(N >= 0 && N < kMaxIndex && K >= 0 && K % 8 == 0 && K < kMaxIndex, MX_ERR_SHAPE,
              "%s: N (%lld), K (%lld, a multiple of 8)", fn, (long long)N, (long long)K);
   if (N == 0 || K == 0) return MX_OK;
-  MX_CHECK(check_tiles(fn, E * ((N + 255) / 256), K));
+  mxk::B128GemmArgs a{};
+  a.qa = qg; a.qb = qx; a.sa = sg; a.sb = sx; a.M = N; a.N = K; a.K = cap; a.ldo = K;
+  a.out_f32 = out_dtype == MX_F32; a.out = out; a.offs = offs; a.E = E; a.dev_err = dev_err;
+  MX_CHECK(check_grid(fn, mxk::b128_wgrad_grid(a)));
   if (cap) {
     MX_CHECK(check_operand(fn, "G", qg, sg, cap, cap / 128 * N));
     MX_CHECK(check_operand(fn, "X", qx, sx, cap, cap / 128 * K));
@@ -353,9 +356,6 @@ mx_status mx_b128_grouped_mm_wgrad(const uint8_t* qg, const float* sg, const uin
   MX_REQUIRE(out, MX_ERR_NULL, "%s: out is NULL", fn);
   MX_REQUIRE(al16(out) && al4(dev_err), MX_ERR_ALIGN, "%s: out must be 16-byte and dev_err 4-byte aligned", fn);
   MX_DEVICE();
-  mxk::B128GemmArgs a{};
-  a.qa = qg; a.qb = qx; a.sa = sg; a.sb = sx; a.M = N; a.N = K; a.K = cap; a.ldo = K;
-  a.out_f32 = out_dtype == MX_F32; a.out = out; a.offs = offs; a.E = E; a.dev_err = dev_err;
   return launched(mxk::launch_b128_wgrad(a, as_stream(stream)), fn);
 }
 
