@@ -26,6 +26,7 @@ needs no padding to run forward, so a few tokens cost the rows that they have.
 import torch
 
 from . import b128, moe, mx
+from .lm import _matrix, _rows
 
 _RECIPES = ("mxfp8", "b128")
 
@@ -39,12 +40,19 @@ class MoELayer:
     def __init__(self, w13, w2, top, recipe="mxfp8", bias=None, **routing):
         if recipe not in _RECIPES:
             raise mx.MXError(f"recipe: {recipe!r}, expected 'mxfp8' or 'b128'")
+        if not isinstance(w2, torch.Tensor) or w2.dim() != 3:
+            raise mx.MXError("w2: expected a tensor [E, D, H]")
         self.E, self.D, self.H = w2.shape
+        if self.D % 128 or self.H % 128:
+            raise mx.MXError(f"w2: D ({self.D}) and H ({self.H}) must be multiples of 128")
         self.top, self.recipe, self.bias, self.routing = top, recipe, bias, routing
         self.set_weights(w13, w2)
 
     def set_weights(self, w13, w2):
         """Quantizes the experts' weights (once an optimizer step)."""
+        for w, name, shape in ((w2, "w2", (self.E, self.D, self.H)), (w13, "w13", (self.E, 2 * self.H, self.D))):
+            if not isinstance(w, torch.Tensor) or w.dtype is not torch.bfloat16 or w.shape != shape:
+                raise mx.MXError(f"{name}: expected a bf16 tensor of shape {shape}")
         if self.recipe == "b128":
             self.q13, self.q2 = b128.quantize_weight(w13), b128.quantize_weight(w2)
         else:
@@ -70,6 +78,13 @@ class MoELayer:
     def forward(self, x, logits, r=None, train=False):
         """x bf16 [T, D], logits bf16 or float32 [T, E], r bf16 [T, D] or None
         (added to the output). Returns (out bf16 [T, D], what backward takes)."""
+        T = _matrix(x, "x")[0]
+        _rows(x, "x", torch.bfloat16, (T, self.D))
+        # a token without logits or without x, or an expert without weights, would drop out unseen
+        if _matrix(logits, "logits", (torch.bfloat16, torch.float32)) != (T, self.E):
+            raise mx.MXError(f"logits: shape {tuple(logits.shape)}, expected {(T, self.E)}")
+        if r is not None:
+            _rows(r, "r", torch.bfloat16, (T, self.D))
         f = moe.route(logits, self.top, bias=self.bias, **self.routing)
         plan = moe.dispatch(f["idx"], self.E, multiple=128 if train or self.recipe == "mxfp8" else 1)
         xq = self._gather(x, plan["src"], train=train)
@@ -91,6 +106,9 @@ class MoELayer:
         """Gradients for dout bf16 [T, D], c from forward(train=True): a dict with
         dx (bf16; r's gradient is dout itself), dlogits (of the logits' type), dw13 and dw2
         (float32)."""
+        if "q_col" not in c["xq"]:
+            raise mx.MXError("backward: c comes from a forward without train=True")
+        _rows(dout, "dout", torch.bfloat16, c["x"].shape)
         H, offs = self.H, c["offs"]
         kw = {k: v for k, v in self.routing.items() if k in ("score", "renorm", "scale")}
         dlogits = moe.route_bwd(c["logits"], c["idx"], moe.combine_bwd(dout, c["y"], c["pos"]), **kw)
