@@ -16,7 +16,9 @@
  *
  * The conventions of mxfp8.h hold (device pointers, row-major tensors, streams,
  * alignment, errors, no allocation, no synchronization). Float32 arrays are
- * 4-byte aligned unless stated. Results do not change from run to run.
+ * 4-byte aligned unless stated, row strides of bf16 matrices at most 2^26 elements,
+ * numbers of rows and capacities below 2^31 - 2^16 where no other bound is given.
+ * Results do not change from run to run.
  *
  * A "slot" is a token's j-th choice: slot t * top + j.
  *
@@ -44,7 +46,8 @@ typedef enum { MX_B128_F32 = 0, MX_B128_RCEIL = 1 } mx_b128_mode;
 
 /* Routing. x: logits [rows, experts] of x_dtype (MX_BF16 or MX_F32), row stride
  * ld >= experts, aligned to its element.
- *   s = float32(softmax(x)) or float32(sigmoid(x)), the nearest float32
+ *   s = float32(softmax(x)) or float32(sigmoid(x)), rounded once from float64 values
+ *       off by some 2^-50: the nearest float32 but for about one score in 2^25
  *   c = float32(s + bias)            (c = s if bias is NULL; float32 [experts])
  * An expert whose logit or c is -infinity is ruled out. With groups > 1 the
  * experts form that many groups of equal size in order; a group's value is its
@@ -143,7 +146,8 @@ mx_status mx_b128_quantize(const void* x, int64_t ld, int64_t rows, int64_t cols
 
 /* B128 of weights, bf16 [batch, rows, cols], in blocks of 128 x 128: q [batch,
  * rows, cols], s; and, unless q_t is NULL, the transposed copies q_t [batch,
- * cols, rows], s_t (the same numbers). rows, cols multiples of 16, at most 2^24. */
+ * cols, rows], s_t (the same numbers). rows, cols multiples of 16, at most 2^24; at most
+ * 2^22 blocks in all. */
 mx_status mx_b128_quantize_weight(const void* w, int64_t batch, int64_t rows,
                                   int64_t cols, mx_b128_mode mode, uint8_t* q,
                                   float* s, uint8_t* q_t, float* s_t,

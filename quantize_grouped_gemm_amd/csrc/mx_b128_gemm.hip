@@ -18,8 +18,9 @@
 // Large products are bound by power as much as by issue: the clock falls to 2.0 GHz
 // while the matrix unit is busy 55% and the vector unit 37% of the time. 65536 rows
 // to 32 experts of 4096 x 7168 1824 us (2.1 PFLOP/s), the weight gradient 7168 x 2048
-// from as many rows 1153 us (1.7), 8192 x 8192 x 8192 440 us (2.5); the products
-// with scales in the matrix unit reach 2.2 to 2.7 on this card.
+// from as many rows 1103 to 1153 us (1.7; float32 results 1257), 8192 x 8192 x 8192 440 us
+// (2.5; with 1 x 128 scales on both sides 524); the products with scales in the matrix
+// unit reach 2.2 to 2.7 on this card.
 //
 // The matrix unit holds groups of 8 products to 2^-13 of the largest, which leaves
 // float32 results off by 1.5e-5 of their size (root mean square).
@@ -858,8 +859,9 @@ static auto with_grouped(const B128GemmArgs& a, Fn f) {
     if (a.M <= 4 * active && columns > kMidColumns && columns < 2 * kWideColumns) return split(FewWide{});
     if (columns < kWideColumns) return split(Mid{});
   }
-  // Large tiles for 128 rows a group and more, if they give half of the CUs one, and some more rows where they give
-  // no more than that. us of Small / Big: 32 x 128 x 4096 x 7168 254, 221; 32 x 100 x 7168 x 2048 122, 128; 8 x 128 x
+  // Large tiles for 128 rows a group and more, if they give half of the CUs one and have rows enough: their time hardly
+  // depends on how many they hold. Rows a group times large tiles says how much there is to share out; from 16384 (the
+  // third example) to 28672 (the fifth) the order turns. us of Small / Big: 32 x 128 x 4096 x 7168 254, 221; 32 x 100 x 7168 x 2048 122, 128; 8 x 128 x
   // 4096 x 7168 66, 87; 8 x 256 x 4096 x 7168 122, 98; 8 x 128 x 7168 x 2048 40, 34; 32 x 256 x 768 x 2048 22, 31;
   // 8 x 512 x 1536 x 7168 82, 92; 8 x 768 x 1536 x 7168 114, 92.
   const int64_t large = std::max(active, a.M / Big::BM) * ((a.N + Big::BN - 1) / Big::BN);
