@@ -28,7 +28,7 @@ def _choice(T, top, E, seed, skew=0.0):
     return torch.multinomial(p.expand(max(T, 1), E), min(top, E), generator=g)[:T].to(I32)
 
 
-# one workgroup (up to 8192 slots) and several chunks, one expert, experts without tokens, one token, none
+# one workgroup (up to 4096 slots) and several chunks, one expert, experts without tokens, one token, none
 PLANS = [(0, 2, 8, 128), (1, 1, 1, 128), (1, 8, 256, 1), (13, 8, 256, 1), (100, 2, 8, 16), (1000, 8, 40, 128),
          (1024, 8, 256, 1), (1025, 8, 256, 128), (1500, 6, 1000, 4), (5000, 2, 1024, 1), (20000, 8, 64, 128),
          (33333, 1, 3, 128), (70000, 4, 17, 7), (262144, 1, 130, 128)]

@@ -35,8 +35,8 @@ def _logits(T, E, dtype, seed, std=1.5, pad=0):
     return (torch.randn((T, E + pad), generator=g) * std).to(dtype)[:, :E], g
 
 
-# every register count and both lane counts (16 lanes a token above 2048 rows),
-# rows of any alignment, one expert and one token
+# every register count with 64 lanes a token (with 16, of more than 16 experts: MANY below and
+# test_gpu_moe_lanes), rows of any alignment, one expert and one token
 SHAPES = [(0, 8, 2), (1, 1, 1), (1, 256, 8), (3, 5, 3), (7, 16, 4), (33, 33, 5), (100, 64, 6), (65, 128, 8), (50, 160, 6),
           (17, 200, 16), (9, 257, 8), (5, 512, 10), (4, 1000, 16), (6, 1024, 8), (2049, 24, 4), (2100, 33, 2),
           (2500, 100, 3), (2064, 256, 8), (2050, 255, 6)]
@@ -186,7 +186,7 @@ def test_repeated_and_on_a_side_stream(gpu):
     assert torch.equal(first["idx"], again["idx"]) and torch.equal(first["weights"], again["weights"])
 
 
-# 16 lanes a token from 4097 (8193 above 128 experts) tokens on: every register count, groups on whole lanes and across them
+# 16 lanes a token from 4097 tokens on: every register count, groups on whole lanes and across them
 MANY = [(4100, 24, 4, 3, 2), (4097, 33, 2, 1, 1), (4101, 64, 6, 8, 3), (4100, 100, 3, 4, 2), (4100, 128, 8, 2, 1),
         (8200, 256, 8, 8, 4), (8197, 255, 6, 5, 3), (8193, 160, 6, 8, 3), (8200, 240, 16, 1, 1)]
 
