@@ -92,9 +92,10 @@ __device__ __forceinline__ uint2 block_codes(uint4 v, const BlockScale& b) {
   return c;
 }
 
-// bf16 of w v rounded once. The float32 product p is off by e = w v - p (exact in
-// one fma), which matters only where p lies on a border of bf16, its lower half
-// 0x8000: one product in 65536, and the least of 16 signed bits, looked for with packed minima.
+// bf16 of w v rounded once. The float32 product p is off by e = w v - p, which
+// matters only where p lies on a border of bf16, its lower half 0x8000: one product in
+// 65536, and the least of 16 signed bits, looked for with packed minima. e is formed in
+// float64, which holds the product; in float32 it would vanish where p is subnormal.
 __device__ __forceinline__ uint4 weigh(uint4 v, float w) {
   float f[8], p[8];
   unpack8(v, f);
@@ -110,8 +111,8 @@ __device__ __forceinline__ uint4 weigh(uint4 v, float w) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t b = __float_as_uint(p[i]);
-      const float e = fmaf(w, f[i], -p[i]);
-      if ((b & 0xFFFFu) == 0x8000u && e != 0.0f) b += (e > 0.0f) == (p[i] > 0.0f) ? 1u : ~0u;
+      const double e = fma((double)w, (double)f[i], -(double)p[i]);
+      if ((b & 0xFFFFu) == 0x8000u && e != 0.0) b += (e > 0.0) == (p[i] > 0.0f) ? 1u : ~0u;
       p[i] = __uint_as_float(b);
     }
   }
